@@ -8,6 +8,8 @@
  *   GEMM1      per expert, [gate | up] = x W1^T, h = silu(gate) * up (SwiGLU);
  *   GEMM2      per expert, y = h W2^T;
  *   combine    per token, out = sum over its k slots of w_j * y_j.
+ * Around it: the norms in front of and behind the block, with its gate and residual
+ * (moe_prenorm, moe_combine_norm), and for the bf16 layer the gradient of every step.
  * The steps follow the fused MoE kernels described on the FlashInfer pull request
  * "[SM90] Add W4A8 MegaMoE support" (dispatch, two expert GEMMs, clamped SwiGLU,
  * top-k reduction), the GEMM + SwiGLU fused MLP of Megatron-LM "Support GEMM +
@@ -85,7 +87,14 @@ enum {
 };
 
 /* Selects which call moe_call_workspace_bytes() sizes the workspace for. */
-enum { MOE_WS_PERMUTE = 0, MOE_WS_GROUPED_FFN = 1, MOE_WS_FORWARD = 2 };
+enum {
+    MOE_WS_PERMUTE = 0,
+    MOE_WS_GROUPED_FFN = 1,
+    MOE_WS_FORWARD = 2,
+    MOE_WS_FFN_BACKWARD = 3, /* 0 bytes for the W4A8 precisions, which have no backward pass */
+    MOE_WS_PRENORM_BACKWARD = 4,
+    MOE_WS_COMBINE_NORM_BACKWARD = 5
+};
 
 typedef struct moe_problem {
     int32_t T;              /* tokens, >= 0 */
@@ -153,8 +162,9 @@ typedef struct moe_weights {
     int32_t w4_layout;
 } moe_weights;
 
-/* Host only.  Bytes of device workspace that serve every entry point for this
- * problem (the largest plan: moe_forward's); 0 if the problem is invalid.  The
+/* Host only.  Bytes of device workspace that serve every entry point of the forward for
+ * this problem (the largest plan: moe_forward's; the backward entry points have their own
+ * sizes in moe_call_workspace_bytes); 0 if the problem is invalid.  The
  * size depends only on the problem, never on the routing, so one allocation made
  * before graph capture serves every call of that shape (the FlashInfer pull request
  * "[SM90] Add W4A8 MegaMoE support" sizes its workspace for the largest plan, and
@@ -164,7 +174,8 @@ size_t moe_workspace_bytes(const moe_problem *p);
 
 /* Host only.  The smaller workspace one step entry point needs (MOE_WS_PERMUTE for
  * moe_permute, MOE_WS_GROUPED_FFN for moe_grouped_ffn, MOE_WS_FORWARD as
- * moe_workspace_bytes); 0 if the problem or `which` is invalid. */
+ * moe_workspace_bytes, MOE_WS_*_BACKWARD for the backward entry points); 0 if the problem or
+ * `which` is invalid. */
 size_t moe_call_workspace_bytes(const moe_problem *p, int which);
 
 /* Host only.  Static English text for a moe_status value. */
@@ -302,6 +313,119 @@ int moe_w4a8_dequant_table(uint8_t *out8, hipStream_t stream);
  * I) when the weights are loaded. */
 int moe_w4a8_tile_weights(const void *codes, const void *bscale, void *codes_tiled, void *bscale_tiled,
                           int32_t E, int32_t N, int32_t K, int32_t prec, hipStream_t stream);
+
+/* ------------------------------------------------------------------ norms around the block
+ * One MoE block of a transformer layer with its norms:
+ *     xn  = rmsnorm(x) * weight                       (moe_prenorm: what is routed and permuted)
+ *     out = scale * residual + gate * rmsnorm(sum_j w_j y_j) * weight      (moe_combine_norm)
+ * and the gradients of both.  Everything here works for every precision: x, residual, out and
+ * the expert outputs are bf16 rows in all of them.  Reductions and intermediate values are
+ * fp32; each output is rounded once, to nearest even.  No atomics: results are reproducible
+ * bit for bit.  With T == 0 the sums over tokens (dweight, a channel gate's dgate, dw1, dw2) are set
+ * to 0 and nothing else happens.  Beyond the checks above, arrays of rows must be 16-byte aligned
+ * (MOE_ERR_UNSUPPORTED otherwise).  An output may not overlap an input unless said so. */
+
+/* RMS norm of a row v of H values: v * rsqrt(mean(v^2) + eps) * weight.  Where a call takes a
+ * `const moe_norm *`, NULL means no norm (the row itself). */
+typedef struct moe_norm {
+    const void *weight; /* bf16 [H], or NULL: ones */
+    float eps;          /* > 0 and finite, so that a row of zeros (a token whose slots are all
+                           dropped) stays a row of zeros; else MOE_ERR_UNSUPPORTED */
+} moe_norm;
+
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+/* The residual stream and the gate of the block's output.  Where a call takes a
+ * `const moe_residual *`, NULL means neither. */
+typedef struct moe_residual {
+    const void *x;      /* bf16 [T][H], or NULL: no residual */
+    float scale;        /* multiplies the residual; finite */
+    const float *gate;  /* fp32 [H] (MOE_GATE_CHANNEL) or [T] (MOE_GATE_TOKEN); unused for MOE_GATE_NONE */
+    int32_t gate_kind;
+} moe_residual;
+
+/* Norm in front of the block: n = norm(x) for x bf16 [T][H].  Writes, each if not NULL,
+ *   xn        bf16 [T][H], n rounded to bf16 (what a router, or a bf16 layer, reads);
+ *   xn8       fp8 E4M3 [T][H] with xn_scale fp32 [T][H/128] (both or neither): the W4A8 layers'
+ *             activations, quantised from the fp32 n: s = amax/448 over 128 columns (1 if the
+ *             amax is 0), code = E4M3(n / s), nearest even.
+ * At least one of them (MOE_ERR_NULL).  With norm == NULL this only quantises x.  xn may be x. */
+int moe_prenorm(const void *x, const moe_norm *norm, const moe_problem *p, void *xn, void *xn8, float *xn_scale,
+                hipStream_t stream);
+
+/* Gradient of moe_prenorm's n with the unpermute of the experts' input gradient folded in:
+ *     dn[t] = sum_{j, slot_row[t*k+j] >= 0} dx_perm[slot_row[t*k+j]] + dxn[t]
+ *     dx[t] = dres[t] + (gradient of the norm at x[t] applied to dn[t])
+ *     dweight = sum_t dn[t] * x[t] * rsqrt(mean(x[t]^2) + eps)
+ * dx_perm bf16 [T*k][H] (with slot_row int32 [T][k]), dxn bf16 [T][H] (what reached n by another
+ * way, e.g. the router) and dres bf16 [T][H] (what reached x by the residual) may each be NULL:
+ * 0; at least one of dx_perm and dxn (MOE_ERR_NULL).  dweight fp32 [H] or NULL, and NULL where
+ * norm is (MOE_ERR_UNSUPPORTED).  norm == NULL: dx = dres + dn, the gradient of moe_permute.
+ * dx bf16 [T][H] may be dres, dxn or x.  Needs ws of moe_call_workspace_bytes(p,
+ * MOE_WS_PRENORM_BACKWARD) bytes if dweight is not NULL (else ws is not used). */
+int moe_prenorm_backward(const void *dx_perm, const int32_t *slot_row, const void *dxn, const void *dres,
+                         const void *x, const moe_norm *norm, const moe_problem *p, void *dx, float *dweight,
+                         void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* moe_unpermute_combine with the norm, gate and residual behind it, in one pass:
+ *     c[t]   = sum_{j, slot_row[t*k+j] >= 0} topk_w[t][j] * y_perm[slot_row[t*k+j]]
+ *     out[t] = bf16( scale * residual[t] + gate * norm(c[t]) )
+ * c is fp32 and never rounded.  out bf16 [T][H] may be the residual.  With norm and residual
+ * NULL the same values as moe_unpermute_combine. */
+int moe_combine_norm(const void *y_perm, const int32_t *slot_row, const float *topk_w, const moe_norm *norm,
+                     const moe_residual *residual, const moe_problem *p, void *out, hipStream_t stream);
+
+/* Gradient of moe_combine_norm for dout bf16 [T][H].  Writes
+ *   dy_perm  bf16 [T*k][H], the rows slot_row names (every slot's row is its own), others untouched;
+ *   dtopk_w  fp32 [T][k] or NULL: dc[t] . y_perm[slot_row], 0 for a dropped slot;
+ *   dresidual bf16 [T][H] or NULL: scale * dout (MOE_ERR_UNSUPPORTED without a residual); may be dout;
+ *   dweight  fp32 [H] or NULL (MOE_ERR_UNSUPPORTED without a norm);
+ *   dgate    fp32 [H] or [T] or NULL (MOE_ERR_UNSUPPORTED without a gate).
+ * c is formed again from y_perm, nothing is kept from the forward.  dy_perm may be y_perm.
+ * Needs ws of moe_call_workspace_bytes(p, MOE_WS_COMBINE_NORM_BACKWARD) bytes if dweight or a
+ * channel gate's dgate is asked for (else ws is not used). */
+int moe_combine_norm_backward(const void *dout, const void *y_perm, const int32_t *slot_row, const float *topk_w,
+                              const moe_norm *norm, const moe_residual *residual, const moe_problem *p,
+                              void *dy_perm, float *dtopk_w, void *dresidual, float *dweight, float *dgate, void *ws,
+                              size_t ws_bytes, hipStream_t stream);
+
+/* moe_forward with moe_combine_norm in the place of its combine: the whole block after
+ * moe_prenorm, for every precision and for MOE_FLAG_SCATTER_Y (not MOE_FLAG_SINGLE_LAUNCH:
+ * MOE_ERR_UNSUPPORTED).  The same workspace as moe_forward; bitwise the step-by-step result. */
+int moe_forward_norm(const float *logits, const uint8_t *slot_drop, const void *x, const float *x_scale,
+                     const moe_weights *w, const moe_norm *norm, const moe_residual *residual, const moe_problem *p,
+                     void *out, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------ training
+ * The gradient of each step of the forward.  moe_unpermute_combine's is
+ * moe_combine_norm_backward with norm and residual NULL, moe_permute's is moe_prenorm_backward
+ * with norm NULL. */
+
+/* Gradient of moe_route_topk: dtopk_w fp32 [T][k] -> dlogits fp32 [T][E].  The chosen experts are
+ * found again from the logits; a slot that slot_drop (or NULL) masks counts as gradient 0 whatever
+ * dtopk_w holds there, and its expert's logit still gets its share (its weight stays in the
+ * softmax).  dlogits is written in full: 0 for the experts not chosen. */
+int moe_route_topk_backward(const float *logits, const uint8_t *slot_drop, const float *dtopk_w, const moe_problem *p,
+                            float *dlogits, hipStream_t stream);
+
+/* moe_grouped_ffn that also keeps what its backward pass needs: gu bf16 [T*k][2I], the
+ * pre-activations x_perm[r] W1_e^T in the order of W1's stored rows, before the clamp.  y_perm is
+ * bitwise moe_grouped_ffn's; the same workspace (MOE_WS_GROUPED_FFN).  MOE_PREC_BF16 only
+ * (MOE_ERR_UNSUPPORTED).  Rows >= offsets[E] of gu and y_perm are not written. */
+int moe_grouped_ffn_train(const void *x_perm, const int32_t *offsets, const moe_weights *w, const moe_problem *p,
+                          void *gu, void *y_perm, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of the grouped FFN.  With s = sigmoid of the clamped gate, for every row r of expert e:
+ *     dh = dy_perm[r] W2_e,   dgate = dh * u * s * (1 + g (1 - s)),   dup = dh * g * s
+ * (g, u clamped; the gradient of a value outside [-clamp, clamp] is 0),
+ *     dx_perm[r] = dgu W1_e,   dw1_e = sum_r dgu^T x_perm[r],   dw2_e = sum_r dy_perm[r]^T h[r].
+ * Writes, each if not NULL, dx_perm bf16 [T*k][H] (rows < offsets[E]), dw1 bf16 [E][2I][H] (in W1's
+ * stored row order) and dw2 bf16 [E][H][I]; an expert without rows gets a gradient of 0.  Products are
+ * bf16 with fp32 accumulation; dgu and h are rounded to bf16 between them.  gu, x_perm and the
+ * weights as for moe_grouped_ffn_train.  MOE_PREC_BF16 only (MOE_ERR_UNSUPPORTED).  Needs ws of
+ * moe_call_workspace_bytes(p, MOE_WS_FFN_BACKWARD) bytes. */
+int moe_grouped_ffn_backward(const void *dy_perm, const void *x_perm, const void *gu, const int32_t *offsets,
+                             const moe_weights *w, const moe_problem *p, void *dx_perm, void *dw1, void *dw2, void *ws,
+                             size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

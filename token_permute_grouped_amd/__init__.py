@@ -21,12 +21,15 @@ MOE_PREC_BF16, MOE_PREC_W4A8, MOE_PREC_W4A8_MX = 0, 1, 2
 PRECISIONS = {"bf16": MOE_PREC_BF16, "w4a8": MOE_PREC_W4A8, "w4a8_mx": MOE_PREC_W4A8_MX}
 MOE_W4_LAYOUT_ROWS, MOE_W4_LAYOUT_TILED = 0, 1
 MOE_WS_PERMUTE, MOE_WS_GROUPED_FFN, MOE_WS_FORWARD = 0, 1, 2
+MOE_WS_FFN_BACKWARD, MOE_WS_PRENORM_BACKWARD, MOE_WS_COMBINE_NORM_BACKWARD = 3, 4, 5
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 
 # every symbol include/moe.h declares
 EXPORTS = (
     "moe_workspace_bytes", "moe_call_workspace_bytes", "moe_status_str", "moe_last_hip_error", "moe_route_topk", "moe_permute",
     "moe_permute_timed", "moe_grouped_ffn", "moe_unpermute_combine", "moe_forward", "moe_forward_timed", "moe_forward_noalloc", "moe_w4a8_dequant_table",
-    "moe_w4a8_tile_weights",
+    "moe_w4a8_tile_weights", "moe_prenorm", "moe_prenorm_backward", "moe_combine_norm", "moe_combine_norm_backward",
+    "moe_forward_norm", "moe_route_topk_backward", "moe_grouped_ffn_train", "moe_grouped_ffn_backward",
 )
 MOE_N_STAGE_EVENTS = 8
 MOE_N_PERMUTE_EVENTS = 3
@@ -54,6 +57,15 @@ class Weights(ctypes.Structure):
     _fields_ = [("w1", ctypes.c_void_p), ("w1_bscale", ctypes.c_void_p), ("w1_gscale", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("w2_bscale", ctypes.c_void_p), ("w2_gscale", ctypes.c_void_p),
                 ("w4_layout", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class Residual(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("scale", ctypes.c_float), ("gate", ctypes.c_void_p),
+                ("gate_kind", ctypes.c_int32)]
 
 
 _lib = None
@@ -91,8 +103,19 @@ def load() -> ctypes.CDLL:
     lib.moe_forward_noalloc.argtypes = [P, P, P, P, PW, PP, P, P]
     lib.moe_w4a8_dequant_table.argtypes = [P, P]
     lib.moe_w4a8_tile_weights.argtypes = [P, P, P, P, I32, I32, I32, I32, P]
+    PN, PR = ctypes.POINTER(Norm), ctypes.POINTER(Residual)
+    lib.moe_prenorm.argtypes = [P, PN, PP, P, P, P, P]
+    lib.moe_prenorm_backward.argtypes = [P, P, P, P, P, PN, PP, P, P, P, SZ, P]
+    lib.moe_combine_norm.argtypes = [P, P, P, PN, PR, PP, P, P]
+    lib.moe_combine_norm_backward.argtypes = [P, P, P, P, PN, PR, PP, P, P, P, P, P, P, SZ, P]
+    lib.moe_forward_norm.argtypes = [P, P, P, P, PW, PN, PR, PP, P, P, SZ, P]
+    lib.moe_route_topk_backward.argtypes = [P, P, P, PP, P, P]
+    lib.moe_grouped_ffn_train.argtypes = [P, P, PW, PP, P, P, P, SZ, P]
+    lib.moe_grouped_ffn_backward.argtypes = [P, P, P, P, PW, PP, P, P, P, P, SZ, P]
     for name in ("moe_route_topk", "moe_permute", "moe_permute_timed", "moe_grouped_ffn", "moe_unpermute_combine", "moe_forward",
-                 "moe_forward_timed", "moe_forward_noalloc", "moe_w4a8_dequant_table", "moe_w4a8_tile_weights"):
+                 "moe_forward_timed", "moe_forward_noalloc", "moe_w4a8_dequant_table", "moe_w4a8_tile_weights",
+                 "moe_prenorm", "moe_prenorm_backward", "moe_combine_norm", "moe_combine_norm_backward",
+                 "moe_forward_norm", "moe_route_topk_backward", "moe_grouped_ffn_train", "moe_grouped_ffn_backward"):
         getattr(lib, name).restype = I32
     _lib = lib
     return lib
@@ -226,3 +249,126 @@ def moe_w4a8_dequant_table(out8, stream=None):
     if _nbytes(out8) < 8 * 16 * 256:
         raise ValueError("moe_w4a8_dequant_table needs an 8*16*256-byte output")
     _check("moe_w4a8_dequant_table", load().moe_w4a8_dequant_table(_ptr(out8), _stream(stream)))
+
+
+# ---------------------------------------------------------------- norms around the block, gradients
+# These also check that every tensor is contiguous and holds the bytes the problem gives it (the
+# library sees pointers only), and run on the device their tensors are on.
+
+def make_norm(weight, eps) -> Norm:
+    """weight: bf16 [H] or None (ones)"""
+    n = Norm(_ptr(weight), eps)
+    n.tensors = lambda p: [(weight, 2 * p.H)]
+    return n
+
+
+def make_residual(x, scale=1.0, gate=None, gate_kind=MOE_GATE_NONE) -> Residual:
+    """x: bf16 [T][H] or None; gate: fp32 [H] (MOE_GATE_CHANNEL) or [T] (MOE_GATE_TOKEN)"""
+    if gate_kind == MOE_GATE_NONE:
+        gate = None
+    r = Residual(_ptr(x), scale, _ptr(gate), gate_kind)
+    r.tensors = lambda p: [(x, 2 * p.T * p.H), (gate, 4 * (p.H if gate_kind == MOE_GATE_CHANNEL else p.T))]
+    return r
+
+
+def _call(fn: str, p: Problem, stream, args, sizes):
+    """Calls `fn` with args (tensors become addresses, descriptors pointers) and the stream.  sizes:
+    (tensor, bytes it has to hold)."""
+    device = None
+    for a in args:
+        if hasattr(a, "tensors"):
+            sizes += a.tensors(p)
+    for t, n in sizes:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: a tensor of shape {tuple(t.shape)} is not contiguous")
+        if _nbytes(t) < n:
+            raise ValueError(f"{fn}: a tensor of shape {tuple(t.shape)} holds {_nbytes(t)} bytes, the problem needs {n}")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{fn}: tensors on {device} and {t.device}")
+    call = getattr(load(), fn)
+    args = [ctypes.byref(a) if isinstance(a, ctypes.Structure) else _ptr(a) for a in args]
+    if device is None or device.type != "cuda":
+        if device is not None and p.T > 0:
+            raise ValueError(f"{fn}: tensors on {device}, not on a GPU")
+        return _check(fn, call(*args, _stream(stream)))
+    import torch
+    if device.index == torch.cuda.current_device():
+        return _check(fn, call(*args, _stream(stream)))
+    with torch.cuda.device(device):
+        return _check(fn, call(*args, _stream(stream)))
+
+
+def _ws_bytes(ws, ws_bytes):
+    return _nbytes(ws) if ws_bytes is None else ws_bytes
+
+
+def moe_prenorm(x, norm, problem: Problem, xn=None, xn8=None, xn_scale=None, stream=None):
+    """norm: make_norm(...) or None"""
+    n = problem.T * problem.H
+    _call("moe_prenorm", problem, stream, [x, norm, problem, xn, xn8, xn_scale],
+          [(x, 2 * n), (xn, 2 * n), (xn8, n), (xn_scale, n // 32)])
+
+
+def moe_prenorm_backward(dx_perm, slot_row, dxn, dres, x, norm, problem: Problem, dx, dweight=None, ws=None,
+                         ws_bytes=None, stream=None):
+    n, S = problem.T * problem.H, problem.T * problem.k
+    _call("moe_prenorm_backward", problem, stream,
+          [dx_perm, slot_row, dxn, dres, x, norm, problem, dx, dweight, ws, _ws_bytes(ws, ws_bytes)],
+          [(dx_perm, 2 * S * problem.H), (slot_row, 4 * S), (dxn, 2 * n), (dres, 2 * n), (x, 2 * n), (dx, 2 * n),
+           (dweight, 4 * problem.H), (ws, 0)])
+
+
+def moe_combine_norm(y_perm, slot_row, topk_w, norm, residual, problem: Problem, out, stream=None):
+    """residual: make_residual(...) or None"""
+    n, S = problem.T * problem.H, problem.T * problem.k
+    _call("moe_combine_norm", problem, stream, [y_perm, slot_row, topk_w, norm, residual, problem, out],
+          [(y_perm, 2 * S * problem.H), (slot_row, 4 * S), (topk_w, 4 * S), (out, 2 * n)])
+
+
+def moe_combine_norm_backward(dout, y_perm, slot_row, topk_w, norm, residual, problem: Problem, dy_perm, dtopk_w=None,
+                              dresidual=None, dweight=None, dgate=None, ws=None, ws_bytes=None, stream=None):
+    n, S = problem.T * problem.H, problem.T * problem.k
+    token_gate = residual is not None and residual.gate_kind == MOE_GATE_TOKEN
+    _call("moe_combine_norm_backward", problem, stream,
+          [dout, y_perm, slot_row, topk_w, norm, residual, problem, dy_perm, dtopk_w, dresidual, dweight, dgate, ws,
+           _ws_bytes(ws, ws_bytes)],
+          [(dout, 2 * n), (y_perm, 2 * S * problem.H), (slot_row, 4 * S), (topk_w, 4 * S), (dy_perm, 2 * S * problem.H),
+           (dtopk_w, 4 * S), (dresidual, 2 * n), (dweight, 4 * problem.H),
+           (dgate, 4 * (problem.T if token_gate else problem.H)), (ws, 0)])
+
+
+def moe_forward_norm(logits, slot_drop, x, x_scale, weights: Weights, norm, residual, problem: Problem, out, ws,
+                     ws_bytes=None, stream=None):
+    T, H, S = problem.T, problem.H, problem.T * problem.k
+    bf16 = problem.prec == MOE_PREC_BF16
+    _call("moe_forward_norm", problem, stream,
+          [logits, slot_drop, x, x_scale, weights, norm, residual, problem, out, ws, _ws_bytes(ws, ws_bytes)],
+          [(logits, 4 * T * problem.E), (slot_drop, S), (x, (2 if bf16 else 1) * T * H),
+           (x_scale, 0 if bf16 else T * H // 32), (out, 2 * T * H), (ws, 0)])
+
+
+def moe_route_topk_backward(logits, slot_drop, dtopk_w, problem: Problem, dlogits, stream=None):
+    n, S = 4 * problem.T * problem.E, problem.T * problem.k
+    _call("moe_route_topk_backward", problem, stream, [logits, slot_drop, dtopk_w, problem, dlogits],
+          [(logits, n), (slot_drop, S), (dtopk_w, 4 * S), (dlogits, n)])
+
+
+def moe_grouped_ffn_train(x_perm, offsets, weights: Weights, problem: Problem, gu, y_perm, ws, ws_bytes=None,
+                          stream=None):
+    n = 2 * problem.T * problem.k * problem.H
+    _call("moe_grouped_ffn_train", problem, stream,
+          [x_perm, offsets, weights, problem, gu, y_perm, ws, _ws_bytes(ws, ws_bytes)],
+          [(x_perm, n), (offsets, 4 * problem.E + 4), (gu, 4 * problem.T * problem.k * problem.I), (y_perm, n), (ws, 0)])
+
+
+def moe_grouped_ffn_backward(dy_perm, x_perm, gu, offsets, weights: Weights, problem: Problem, dx_perm=None, dw1=None,
+                             dw2=None, ws=None, ws_bytes=None, stream=None):
+    n, w = 2 * problem.T * problem.k * problem.H, 2 * problem.E * problem.H * problem.I
+    _call("moe_grouped_ffn_backward", problem, stream,
+          [dy_perm, x_perm, gu, offsets, weights, problem, dx_perm, dw1, dw2, ws, _ws_bytes(ws, ws_bytes)],
+          [(dy_perm, n), (x_perm, n), (gu, 4 * problem.T * problem.k * problem.I), (offsets, 4 * problem.E + 4),
+           (dx_perm, n), (dw1, 2 * w), (dw2, w), (ws, 0)])

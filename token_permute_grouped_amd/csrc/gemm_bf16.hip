@@ -57,21 +57,22 @@
 // the way the FlashInfer split kernels fold dispatch into their first GEMM.  Each
 // 128-byte piece of a row is still one whole cache line, so the loads stay coalesced.
 //
+// Gradients.  dh = dy W2 and dx = dgu W1 are the same loop with the weights read as [K][N] rows: a
+// stage is then 64 weight rows of 256 columns, brought in by the same DMAs, and the weight fragments
+// come through the LDS's transposing reads (load_trans), so no transposed copy of the weights is made
+// (it would cost 4.3 + 8.6 GB of traffic on the skewed layer).  dh stays in fp32 through the gradient
+// of the SwiGLU, which is formed in the epilogue.
+//
 // Scheduling.  The device-side tile list gives the m-tiles (expert, first row);
 // tile_map assigns them to workgroups by band and XCD rectangle (below).
 // Workgroups past the tile count exit before any barrier.
 #include <type_traits>
 
-#include "moe_internal.h"
+#include "gemm_trans.h"
 
 namespace tpg {
 
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBM = kGemmBM;  // token rows per tile (256)
 constexpr int kBN = 256;      // weight rows per tile
@@ -126,28 +127,26 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return pack_bf16x2(a, b);
 }
 
-// one 16-byte-per-lane DMA from a raw buffer straight into LDS (1 KB per wave, lane-linear)
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t soff, void *dst) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
-}
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// LDS barrier without a global-memory fence: register loads stay in flight across it.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// scheduling pattern: NR fragment reads (DS) spread evenly over M MFMAs
-template <int NR, int M, int I = 0>
-__device__ __forceinline__ void interleave_ds_mfma() {
-    if constexpr (I < NR) {
-        constexpr int m = (M * (I + 1)) / NR - (M * I) / NR;
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                       // DS read
-        if constexpr (m > 0) __builtin_amdgcn_sched_group_barrier(0x008, m, 0);  // MFMA
-        interleave_ds_mfma<NR, M, I + 1>();
+// Gradient of h = silu(g) u at the kept pre-activations: dg, du for dh, and h itself.  The clamp is
+// min(max(v, -c), c); its gradient is 0 outside [-c, c] and 1 on the border.
+__device__ __forceinline__ void glu_grad(float g0, float u0, float dh, float clamp, float &dg, float &du, float &h) {
+    float g = g0, u = u0;
+    if (clamp > 0.f) {
+        g = fminf(fmaxf(g, -clamp), clamp);
+        u = fminf(fmaxf(u, -clamp), clamp);
     }
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g)), gs = g * s;
+    h = gs * u;
+    dg = dh * u * (s + gs * (1.0f - s));
+    du = dh * gs;
+    if (clamp > 0.f) {
+        if (fabsf(g0) > clamp) dg = 0.f;
+        if (fabsf(u0) > clamp) du = 0.f;
+    }
+}
+
+__device__ __forceinline__ u32x4 pack8(const float *v) {
+    return (u32x4){pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
 }
 
 // pattern with extra work: per group, X instructions of class `cls`, one DS read, MFMAs
@@ -165,7 +164,16 @@ __device__ __forceinline__ void interleave_x_ds_mfma() {
 
 }  // namespace
 
-template <bool kSwiGLU>
+// The products of the forward and of the backward pass that have the token rows on their rows.
+enum class Gemm {
+    kGlu,      // GEMM1 + SwiGLU -> h
+    kGluKeep,  // the same, with the pre-activations stored too
+    kOut,      // GEMM2 -> y
+    kGradGlu,  // dy W2 = dh, then the gradient of the SwiGLU -> dgu, and h again from the kept gu
+    kGradIn,   // dgu W1 -> dx
+};
+
+template <Gemm kKind>
 __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     const uint16_t *__restrict__ A,        // [S][K] activations in expert-contiguous row order, or
                                            // with row_src: the token rows [a_rows][K]
@@ -177,7 +185,12 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     const int32_t *__restrict__ n_tiles,   // [1]
     int K, int N, int I, int il, float clamp,
     uint16_t *__restrict__ C, int ldc,     // [S][ldc]
-    const int32_t *__restrict__ row_dst) { // NULL, or [S]: row r of the tile order is stored to row row_dst[r] of C
+    const int32_t *__restrict__ row_dst,   // NULL, or [S]: row r of the tile order is stored to row row_dst[r] of C
+    const uint16_t *__restrict__ gu_in,    // kGradGlu: [S][2I] kept pre-activations
+    uint16_t *__restrict__ gu_out) {       // kGluKeep: [S][2I] pre-activations; kGradGlu: their gradients
+    constexpr bool kSwiGLU = kKind == Gemm::kGlu || kKind == Gemm::kGluKeep;
+    // gradients: the weights are read as [E][K][N], their K the row index of the stored matrix
+    constexpr bool kTrans = kKind == Gemm::kGradGlu || kKind == Gemm::kGradIn;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kBBase + kBStages * kBStage];  // 160 KB
 
     // ---- tile of this workgroup: band of m-tiles, XCD rectangle within the band, tile within it
@@ -249,6 +262,13 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     };
 #pragma unroll
     for (int i = 0; i < kOpsB; ++i) {
+        if constexpr (kTrans) {
+            // stage row r: 256 columns of weight row kt * 64 + r (512 bytes, two rows per op)
+            const int r = wave * (kBK / kWaves) + i * 2 + (lane >> 5);
+            const int c = nt * kBN + tchunk(r, lane & 31) * 8;
+            offB[i] = c < N ? (uint32_t)(r * N + c) * 2u : 0x80000000u;  // columns past N: not read
+            continue;
+        }
         const int r = wave * (kBN / kWaves) + i * 8 + (lane >> 3);  // tile weight row
         int wr;
         if (kSwiGLU) {
@@ -281,7 +301,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     auto dmaB = [&](int kt, int bstage, int i0, int n, int BB) {
         unsigned char *dst = lds + BB + bstage * kBStage + wave * (kBN / kWaves) * kRowBytes;
 #pragma unroll
-        for (int i = i0; i < i0 + n; ++i) dma16(rsB, offB[i], kt * kRowBytes, dst + i * 1024);
+        for (int i = i0; i < i0 + n; ++i) dma16(rsB, offB[i], kTrans ? kt * (kBK * 2) * N : kt * kRowBytes, dst + i * 1024);
     };
 
     f32x16 acc[2][4];
@@ -300,7 +320,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     auto mainloop = [&](auto nb_tag, auto sp_tag) {
         constexpr int NB = decltype(nb_tag)::value;
         constexpr bool kSp = decltype(sp_tag)::value;  // sparse tile: at most 64 live rows
-        constexpr int NR = 2 + NB;  // fragment reads per K step
+        constexpr int NR = (kTrans ? 4 : 2) + NB;  // fragment reads per K step
         constexpr int NM = 2 * NB;  // MFMAs per K step
         constexpr int NL = kSp ? 1 : kLoads;            // activation loads per thread and stage
         constexpr int AS = kSp ? kAStageSp : kAStage;
@@ -316,8 +336,12 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
                 const int kc = ks * 2 + fk;
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    const int r = wn * 64 + a * 32 + fr;
-                    fw[buf][a] = __builtin_bit_cast(bf16x8, sb[r * 8 + slot(r, kc)]);
+                    if constexpr (kTrans) {
+                        fw[buf][a] = load_trans(lds + BB + bstage * kBStage, wn * 64 + a * 32, ks, lane);
+                    } else {
+                        const int r = wn * 64 + a * 32 + fr;
+                        fw[buf][a] = __builtin_bit_cast(bf16x8, sb[r * 8 + slot(r, kc)]);
+                    }
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -472,6 +496,81 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     auto cofs = [](int r, int c) { return r * (kCols * 2) + ((c ^ (r & 15)) << 4); };
     const int half = lane >> 5;
     lds_barrier();  // every wave is done with the last stage's operands
+    if constexpr (kKind == Gemm::kGradGlu) {
+        // dh goes through LDS in fp32, 128 columns at a time (wave columns 0, 1, then 2, 3): a row of
+        // 32 chunks of 4 values, chunk c of row r at c ^ (r & 31).  A thread then takes 8 columns of a
+        // row: reads gate and up, writes both gradients and h, each 16 bytes.
+#pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+            if ((wn >> 1) == p) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int tr = wm * 128 + b * 32 + (lane & 31);
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+#pragma unroll
+                        for (int g4 = 0; g4 < 4; ++g4) {
+                            const int c = (wn & 1) * 16 + a * 8 + g4 * 2 + half;
+                            *(f32x4 *)(lds + tr * 512 + ((c ^ (tr & 31)) << 4)) =
+                                (f32x4){acc[a][b][g4 * 4], acc[a][b][g4 * 4 + 1], acc[a][b][g4 * 4 + 2],
+                                        acc[a][b][g4 * 4 + 3]};
+                        }
+                }
+            }
+            lds_barrier();
+            const int c8 = tid & 15;                       // 8-column group of this thread
+            const int col = nt * kBN + p * 128 + c8 * 8;   // hidden column
+            const int gcol = il == 0 ? col : col / il * 2 * il + col % il, ucol = gcol + (il == 0 ? I : il);
+            if (col < N) {
+                for (int tr = tid >> 4; tr < rows; tr += kThreads / 16) {
+                    const int64_t r = row_begin + tr;
+                    const u32x4 gv = *(const u32x4 *)(gu_in + r * 2 * I + gcol);
+                    const u32x4 uv = *(const u32x4 *)(gu_in + r * 2 * I + ucol);
+                    const f32x4 d0 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2) ^ (tr & 31)) << 4));
+                    const f32x4 d1 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2 + 1) ^ (tr & 31)) << 4));
+                    float dg[8], du[8], hv[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float g = __uint_as_float(q & 1 ? gv[q >> 1] & 0xffff0000u : gv[q >> 1] << 16);
+                        const float u = __uint_as_float(q & 1 ? uv[q >> 1] & 0xffff0000u : uv[q >> 1] << 16);
+                        glu_grad(g, u, q < 4 ? d0[q & 3] : d1[q & 3], clamp, dg[q], du[q], hv[q]);
+                    }
+                    *(u32x4 *)(gu_out + r * 2 * I + gcol) = pack8(dg);
+                    *(u32x4 *)(gu_out + r * 2 * I + ucol) = pack8(du);
+                    *(u32x4 *)(C + r * ldc + col) = pack8(hv);
+                }
+            }
+            lds_barrier();
+        }
+        return;
+    }
+    if constexpr (kKind == Gemm::kGluKeep) {
+        // the pre-activations first, a 256-column bf16 tile in W1's stored row order: a contiguous
+        // run of 256 (interleaved rows), or 128 gate and 128 up columns I apart
+        auto gofs = [](int r, int c) { return r * (kBN * 2) + ((c ^ (r & 15)) << 4); };
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int tr = wm * 128 + b * 32 + (lane & 31);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int g4 = 0; g4 < 4; ++g4) {
+                    u32x2 o;
+                    o.x = pack2(acc[a][b][g4 * 4 + 0], acc[a][b][g4 * 4 + 1]);
+                    o.y = pack2(acc[a][b][g4 * 4 + 2], acc[a][b][g4 * 4 + 3]);
+                    *(u32x2 *)(lds + gofs(tr, wn * 8 + a * 4 + g4) + half * 8) = o;
+                }
+        }
+        lds_barrier();
+        const int c = lane & 31, i16 = c & 15;
+        const int tc = il == 0 ? (i16 >> 2) * 8 + (c >> 4) * 4 + (i16 & 3) : c;  // 16-byte chunk of the tile row
+        const int gc = il == 0 ? (c >> 4) * I + nt * (kBN / 2) + i16 * 8 : nt * kBN + c * 8;  // stored column
+#pragma unroll 4
+        for (int tr = wave * 2 + half; tr < kBM; tr += kWaves * 2)
+            if (tr < rows)
+                *(u32x4 *)(gu_out + (int64_t)(row_begin + tr) * 2 * I + gc) = *(const u32x4 *)(lds + gofs(tr, tc));
+        lds_barrier();
+    }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         const int tr = wm * 128 + b * 32 + (lane & 31);
@@ -514,24 +613,28 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
 }
 
 namespace {
-template <bool kSwiGLU>
+template <Gemm kKind>
 hipError_t launch(const uint16_t *A, const int32_t *row_src, int gather_k, int a_rows, const uint16_t *W,
                   const int32_t *offsets, const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int K,
-                  int N, int I, int il, float clamp, uint16_t *C, int ldc, const int32_t *row_dst, hipStream_t s) {
+                  int N, int I, int il, float clamp, uint16_t *C, int ldc, const int32_t *row_dst, hipStream_t s,
+                  const uint16_t *gu_in = nullptr, uint16_t *gu_out = nullptr) {
     const int nb_n = (N + kBN - 1) / kBN;
     const TileMap tm = tile_map(nb_n);
     const int64_t blocks = (max_tiles + tm.gm - 1) / tm.gm * tm.per_band;
-    hipLaunchKernelGGL(grouped_gemm_bf16_kernel<kSwiGLU>, dim3(blocks), dim3(kThreads), 0, s, A, row_src, gather_k,
-                       a_rows, W, offsets, tiles, n_tiles, K, N, I, il, clamp, C, ldc, row_dst);
+    hipLaunchKernelGGL(grouped_gemm_bf16_kernel<kKind>, dim3(blocks), dim3(kThreads), 0, s, A, row_src, gather_k,
+                       a_rows, W, offsets, tiles, n_tiles, K, N, I, il, clamp, C, ldc, row_dst, gu_in, gu_out);
     return hipGetLastError();
 }
 }  // namespace
 
 hipError_t launch_gemm1_swiglu_bf16(const uint16_t *x_perm, const uint16_t *w1, const int32_t *offsets,
                                     const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
-                                    int glu_interleave, float clamp, uint16_t *h, hipStream_t s) {
-    return launch<true>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I, glu_interleave,
-                        clamp, h, I, nullptr, s);
+                                    int glu_interleave, float clamp, uint16_t *h, uint16_t *gu, hipStream_t s) {
+    if (gu)
+        return launch<Gemm::kGluKeep>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
+                                      glu_interleave, clamp, h, I, nullptr, s, nullptr, gu);
+    return launch<Gemm::kGlu>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
+                              glu_interleave, clamp, h, I, nullptr, s);
 }
 
 hipError_t launch_gemm1_swiglu_gather_bf16(const uint16_t *x, const int32_t *row_src, int T, int k,
@@ -539,15 +642,28 @@ hipError_t launch_gemm1_swiglu_gather_bf16(const uint16_t *x, const int32_t *row
                                            const int32_t *n_tiles, int64_t max_tiles, int H, int I,
                                            int glu_interleave, float clamp, uint16_t *h, hipStream_t s) {
     if (!gather_fits(T, H)) return hipErrorInvalidValue;
-    return launch<true>(x, row_src, k, T, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I, glu_interleave, clamp,
-                        h, I, nullptr, s);
+    return launch<Gemm::kGlu>(x, row_src, k, T, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I, glu_interleave,
+                              clamp, h, I, nullptr, s);
 }
 
 hipError_t launch_gemm2_bf16(const uint16_t *h, const uint16_t *w2, const int32_t *offsets, const int32_t *tiles,
                              const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *y_perm,
                              const int32_t *row_dst, hipStream_t s) {
-    return launch<false>(h, nullptr, 1, 0, w2, offsets, tiles, n_tiles, max_tiles, I, H, I, 0, 0.0f, y_perm, H, row_dst,
-                         s);
+    return launch<Gemm::kOut>(h, nullptr, 1, 0, w2, offsets, tiles, n_tiles, max_tiles, I, H, I, 0, 0.0f, y_perm, H,
+                              row_dst, s);
+}
+
+hipError_t launch_grad_glu_bf16(const uint16_t *dy, const uint16_t *w2, const uint16_t *gu, const int32_t *offsets,
+                                const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
+                                int glu_interleave, float clamp, uint16_t *dgu, uint16_t *h, hipStream_t s) {
+    return launch<Gemm::kGradGlu>(dy, nullptr, 1, 0, w2, offsets, tiles, n_tiles, max_tiles, H, I, I, glu_interleave,
+                                  clamp, h, I, nullptr, s, gu, dgu);
+}
+
+hipError_t launch_grad_in_bf16(const uint16_t *dgu, const uint16_t *w1, const int32_t *offsets, const int32_t *tiles,
+                               const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *dx, hipStream_t s) {
+    return launch<Gemm::kGradIn>(dgu, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, 2 * I, H, I, 0, 0.0f, dx,
+                                 H, nullptr, s);
 }
 
 }  // namespace tpg

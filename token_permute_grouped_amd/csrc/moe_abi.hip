@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "block_norm.h"
 #include "moe_internal.h"
 
 // Scratch of moe_forward_noalloc: one array per GPU the library runs on (each holds it until the
@@ -55,6 +56,59 @@ int check_weights(const moe_weights *w, const moe_problem *p) {
     if (is_w4a8(p) && w->w4_layout != MOE_W4_LAYOUT_ROWS && w->w4_layout != MOE_W4_LAYOUT_TILED)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
+}
+
+// arrays of rows that the kernels of the norms and of the backward pass read or write 16 bytes at a time
+template <typename... P>
+int check_aligned(P... ptr) {
+    return ((((uintptr_t)ptr) | ...) & 15) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+int check_norm(const moe_norm *n) {
+    if (!n) return MOE_OK;
+    if (!(n->eps >= 1.17549435e-38f) || n->eps > 3.0e38f) return MOE_ERR_UNSUPPORTED;  // also rejects NaN
+    return check_aligned(n->weight);
+}
+
+int check_residual(const moe_residual *r) {
+    if (!r) return MOE_OK;
+    if (r->gate_kind != MOE_GATE_NONE && r->gate_kind != MOE_GATE_CHANNEL && r->gate_kind != MOE_GATE_TOKEN)
+        return MOE_ERR_UNSUPPORTED;
+    if (r->gate_kind != MOE_GATE_NONE && !r->gate) return MOE_ERR_NULL;
+    if (r->x && !(r->scale >= -3.4028235e38f && r->scale <= 3.4028235e38f)) return MOE_ERR_UNSUPPORTED;
+    return check_aligned(r->x, r->gate_kind == MOE_GATE_CHANNEL ? r->gate : nullptr);
+}
+
+// partial rows of one sum over tokens
+size_t partial_bytes(const moe_problem &p) { return align256((size_t)norm_partials(p) * p.H * 4); }
+
+// without tokens a sum over tokens is 0
+int set_zero(void *dst, size_t bytes, hipStream_t s) {
+    if (!dst) return MOE_OK;
+    const int st = check_aligned(dst);
+    return st ? st : hip_status(launch_zero(dst, bytes, s));
+}
+
+// workspace of moe_grouped_ffn_backward
+struct BackwardLayout {
+    size_t tiles, n_tiles, order, dgu, h, end;
+};
+BackwardLayout backward_layout(const moe_problem &p) {
+    BackwardLayout L;
+    const size_t S = (size_t)n_slots(p);
+    size_t o = 0;
+    L.tiles = o;
+    o = align256(o + (size_t)max_m_tiles(p) * 2 * 4);
+    L.n_tiles = o;
+    o = align256(o + 16);
+    L.order = o;
+    o = align256(o + (size_t)p.E * 4);
+    L.dgu = o;
+    o = align256(o + S * 2 * (size_t)p.I * 2);
+    L.h = o;
+    o = align256(o + S * (size_t)p.I * 2);
+    L.end = o;
+    return L;
 }
 
 }  // namespace
@@ -123,7 +177,7 @@ int run_permute(const void *x, const float *x_scale, const int32_t *topk_idx, co
 }
 
 int run_grouped_ffn(const void *x_perm, const float *x_perm_scale, const int32_t *offsets, const moe_weights &w,
-                    const moe_problem &p, void *y_perm, char *ws, hipStream_t s) {
+                    const moe_problem &p, void *y_perm, char *ws, hipStream_t s, void *gu = nullptr) {
     const WsLayout L = ws_layout(p);
     int32_t *tiles = (int32_t *)(ws + L.tiles);
     int32_t *n_tiles = (int32_t *)(ws + L.n_tiles);
@@ -137,15 +191,22 @@ int run_grouped_ffn(const void *x_perm, const float *x_perm_scale, const int32_t
                                                   (uint16_t *)y_perm, nullptr, s));
     uint16_t *h = (uint16_t *)(ws + L.h);
     st = hip_status(launch_gemm1_swiglu_bf16((const uint16_t *)x_perm, (const uint16_t *)w.w1, offsets, tiles,
-                                             n_tiles, max_tiles, p.H, p.I, p.glu_interleave, p.swiglu_clamp, h, s));
+                                             n_tiles, max_tiles, p.H, p.I, p.glu_interleave, p.swiglu_clamp, h,
+                                             (uint16_t *)gu, s));
     if (st) return st;
     return hip_status(launch_gemm2_bf16(h, (const uint16_t *)w.w2, offsets, tiles, n_tiles, max_tiles, p.H, p.I,
                                         (uint16_t *)y_perm, nullptr, s));
 }
 
+// the norm, gate and residual that moe_forward_norm puts in the place of the plain combine
+struct BlockEnd {
+    const moe_norm *norm;
+    const moe_residual *residual;
+};
+
 int forward_impl(const float *logits, const uint8_t *slot_drop, const void *x, const float *x_scale,
                  const moe_weights *w, const moe_problem *p, void *out, void *ws, size_t ws_bytes, hipStream_t stream,
-                 void *const *ev) {
+                 void *const *ev, const BlockEnd *end = nullptr) {
     int st = check_problem(p);
     if (st) return st;
     if (p->T == 0) return MOE_OK;
@@ -173,6 +234,7 @@ int forward_impl(const float *logits, const uint8_t *slot_drop, const void *x, c
     };
     const bool w4 = is_w4a8(p);
     if (p->flags & MOE_FLAG_SINGLE_LAUNCH) {
+        if (end) return MOE_ERR_UNSUPPORTED;
         if (!w4 || !forward_small_w4a8_fits(*p)) return MOE_ERR_UNSUPPORTED;
         // the whole forward in one launch: its stages have no marks of their own (0-4 before it,
         // 5-7 after it)
@@ -235,7 +297,7 @@ int forward_impl(const float *logits, const uint8_t *slot_drop, const void *x, c
         else
             st = hip_status(launch_gemm1_swiglu_bf16((const uint16_t *)x_perm, (const uint16_t *)w->w1, offsets,
                                                      tiles, n_tiles, max_tiles, p->H, p->I, p->glu_interleave,
-                                                     p->swiglu_clamp, h, s));
+                                                     p->swiglu_clamp, h, nullptr, s));
         if (st) return st;
         if ((st = mark(5))) return st;
         if ((st = hip_status(launch_gemm2_bf16(h, (const uint16_t *)w->w2, offsets, tiles, n_tiles, max_tiles, p->H,
@@ -243,9 +305,13 @@ int forward_impl(const float *logits, const uint8_t *slot_drop, const void *x, c
             return st;
     }
     if ((st = mark(6))) return st;
-    if ((st = hip_status(launch_combine((const uint16_t *)y_perm, slot_row, topk_w, p->T, p->k, p->H, scatter,
-                                        (uint16_t *)out, s))))
-        return st;
+    if (end)
+        st = hip_status(launch_combine_norm((const uint16_t *)y_perm, slot_row, topk_w, end->norm, end->residual, *p,
+                                            scatter, (uint16_t *)out, s));
+    else
+        st = hip_status(launch_combine((const uint16_t *)y_perm, slot_row, topk_w, p->T, p->k, p->H, scatter,
+                                       (uint16_t *)out, s));
+    if (st) return st;
     return mark(7);
 }
 
@@ -269,6 +335,9 @@ size_t moe_call_workspace_bytes(const moe_problem *p, int which) {
         case MOE_WS_PERMUTE: return L.permute_end;
         case MOE_WS_GROUPED_FFN: return L.ffn_end;
         case MOE_WS_FORWARD: return L.forward_end;
+        case MOE_WS_FFN_BACKWARD: return p->prec == MOE_PREC_BF16 ? backward_layout(*p).end : 0;
+        case MOE_WS_PRENORM_BACKWARD: return partial_bytes(*p);
+        case MOE_WS_COMBINE_NORM_BACKWARD: return 2 * partial_bytes(*p);
         default: return 0;
     }
 }
@@ -405,6 +474,138 @@ int moe_forward_noalloc(const float *logits, const uint8_t *slot_drop, const voi
     void *ws = nullptr;
     if ((st = scratch_address(stream, &ws))) return st;
     return forward_impl(logits, slot_drop, x, x_scale, w, p, out, ws, MOE_NOALLOC_SCRATCH_BYTES, stream, nullptr);
+}
+
+int moe_forward_norm(const float *logits, const uint8_t *slot_drop, const void *x, const float *x_scale,
+                     const moe_weights *w, const moe_norm *norm, const moe_residual *residual, const moe_problem *p,
+                     void *out, void *ws, size_t ws_bytes, hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->T == 0) return MOE_OK;
+    if ((st = check_norm(norm)) || (st = check_residual(residual)) || (st = check_aligned(out))) return st;
+    const BlockEnd end{norm, residual};
+    return forward_impl(logits, slot_drop, x, x_scale, w, p, out, ws, ws_bytes, stream, nullptr, &end);
+}
+
+int moe_prenorm(const void *x, const moe_norm *norm, const moe_problem *p, void *xn, void *xn8, float *xn_scale,
+                hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->T == 0) return MOE_OK;
+    if (!x || (!xn && !xn8) || !xn8 != !xn_scale) return MOE_ERR_NULL;
+    if ((st = check_norm(norm)) || (st = check_aligned(x, xn, xn8))) return st;
+    return hip_status(launch_prenorm(x, norm, *p, xn, xn8, xn_scale, stream));
+}
+
+int moe_prenorm_backward(const void *dx_perm, const int32_t *slot_row, const void *dxn, const void *dres,
+                         const void *x, const moe_norm *norm, const moe_problem *p, void *dx, float *dweight,
+                         void *ws, size_t ws_bytes, hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->T == 0) return set_zero(dweight, (size_t)p->H * 4, stream);
+    if (!dx || (!dx_perm && !dxn) || (dx_perm && !slot_row) || (norm && !x)) return MOE_ERR_NULL;
+    if (dweight && !norm) return MOE_ERR_UNSUPPORTED;
+    if (dweight && !ws) return MOE_ERR_NULL;
+    if ((st = check_norm(norm)) || (st = check_aligned(dx_perm, dxn, dres, norm ? x : nullptr, dx, dweight, ws)))
+        return st;
+    if (dweight && ws_bytes < partial_bytes(*p)) return MOE_ERR_WORKSPACE;
+    return hip_status(launch_prenorm_backward(dx_perm, slot_row, dxn, dres, x, norm, *p, dx, dweight, (float *)ws,
+                                              stream));
+}
+
+int moe_combine_norm(const void *y_perm, const int32_t *slot_row, const float *topk_w, const moe_norm *norm,
+                     const moe_residual *residual, const moe_problem *p, void *out, hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->T == 0) return MOE_OK;
+    if (!y_perm || !slot_row || !topk_w || !out) return MOE_ERR_NULL;
+    if ((st = check_norm(norm)) || (st = check_residual(residual)) || (st = check_aligned(y_perm, out))) return st;
+    return hip_status(launch_combine_norm((const uint16_t *)y_perm, slot_row, topk_w, norm, residual, *p, false,
+                                          (uint16_t *)out, stream));
+}
+
+int moe_combine_norm_backward(const void *dout, const void *y_perm, const int32_t *slot_row, const float *topk_w,
+                              const moe_norm *norm, const moe_residual *residual, const moe_problem *p,
+                              void *dy_perm, float *dtopk_w, void *dresidual, float *dweight, float *dgate, void *ws,
+                              size_t ws_bytes, hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->T == 0) {
+        if ((st = set_zero(dweight, (size_t)p->H * 4, stream))) return st;
+        return residual && residual->gate_kind == MOE_GATE_CHANNEL ? set_zero(dgate, (size_t)p->H * 4, stream) : MOE_OK;
+    }
+    if (!dout || !y_perm || !slot_row || !topk_w || !dy_perm) return MOE_ERR_NULL;
+    if ((st = check_norm(norm)) || (st = check_residual(residual))) return st;
+    const int gate_kind = residual ? residual->gate_kind : MOE_GATE_NONE;
+    if ((dweight && !norm) || (dgate && gate_kind == MOE_GATE_NONE) || (dresidual && !(residual && residual->x)))
+        return MOE_ERR_UNSUPPORTED;
+    const bool partials = dweight || (dgate && gate_kind == MOE_GATE_CHANNEL);
+    if (partials && !ws) return MOE_ERR_NULL;
+    if ((st = check_aligned(dout, y_perm, dy_perm, dresidual, ws))) return st;
+    if (partials && ws_bytes < 2 * partial_bytes(*p)) return MOE_ERR_WORKSPACE;
+    return hip_status(launch_combine_norm_backward(dout, y_perm, slot_row, topk_w, norm, residual, *p, dy_perm, dtopk_w,
+                                                   dresidual, dweight, dgate, (float *)ws, stream));
+}
+
+int moe_route_topk_backward(const float *logits, const uint8_t *slot_drop, const float *dtopk_w, const moe_problem *p,
+                            float *dlogits, hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->T == 0) return MOE_OK;
+    if (!logits || !dtopk_w || !dlogits) return MOE_ERR_NULL;
+    return hip_status(launch_route_topk_backward(logits, slot_drop, dtopk_w, p->T, p->E, p->k, dlogits, stream));
+}
+
+int moe_grouped_ffn_train(const void *x_perm, const int32_t *offsets, const moe_weights *w, const moe_problem *p,
+                          void *gu, void *y_perm, void *ws, size_t ws_bytes, hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->prec != MOE_PREC_BF16) return MOE_ERR_UNSUPPORTED;
+    if (p->T == 0) return MOE_OK;
+    if (!x_perm || !offsets || !gu || !y_perm || !ws) return MOE_ERR_NULL;
+    if ((st = check_weights(w, p)) || (st = check_aligned(x_perm, w->w1, w->w2, gu, y_perm, ws))) return st;
+    if (ws_bytes < moe_call_workspace_bytes(p, MOE_WS_GROUPED_FFN)) return MOE_ERR_WORKSPACE;
+    return run_grouped_ffn(x_perm, nullptr, offsets, *w, *p, y_perm, (char *)ws, stream, gu);
+}
+
+int moe_grouped_ffn_backward(const void *dy_perm, const void *x_perm, const void *gu, const int32_t *offsets,
+                             const moe_weights *w, const moe_problem *p, void *dx_perm, void *dw1, void *dw2, void *ws,
+                             size_t ws_bytes, hipStream_t stream) {
+    int st = check_problem(p);
+    if (st) return st;
+    if (p->prec != MOE_PREC_BF16) return MOE_ERR_UNSUPPORTED;
+    if (p->T == 0) {
+        const size_t n = (size_t)p->E * p->H * p->I * 2;  // bytes of dw2, half of dw1's
+        if ((st = set_zero(dw1, 2 * n, stream))) return st;
+        return set_zero(dw2, n, stream);
+    }
+    if (!dy_perm || !gu || !offsets || !ws || (!dx_perm && !dw1 && !dw2) || (dw1 && !x_perm)) return MOE_ERR_NULL;
+    if ((st = check_weights(w, p)) ||
+        (st = check_aligned(dy_perm, dw1 ? x_perm : nullptr, gu, w->w1, w->w2, dx_perm, dw1, dw2, ws)))
+        return st;
+    if (ws_bytes < moe_call_workspace_bytes(p, MOE_WS_FFN_BACKWARD)) return MOE_ERR_WORKSPACE;
+    const BackwardLayout L = backward_layout(*p);
+    char *b = (char *)ws;
+    int32_t *tiles = (int32_t *)(b + L.tiles), *n_tiles = (int32_t *)(b + L.n_tiles);
+    int32_t *order = (int32_t *)(b + L.order);
+    uint16_t *dgu = (uint16_t *)(b + L.dgu), *h = (uint16_t *)(b + L.h);
+    const int64_t max_tiles = max_m_tiles(*p);
+    st = hip_status(launch_build_tiles(offsets, p->E, gemm_bm(*p), tile_order(*p), tiles, n_tiles, stream));
+    if (!st && (dw1 || dw2)) st = hip_status(launch_expert_order(offsets, p->E, order, stream));
+    if (!st)
+        st = hip_status(launch_grad_glu_bf16((const uint16_t *)dy_perm, (const uint16_t *)w->w2, (const uint16_t *)gu,
+                                             offsets, tiles, n_tiles, max_tiles, p->H, p->I, p->glu_interleave,
+                                             p->swiglu_clamp, dgu, h, stream));
+    if (!st && dx_perm)
+        st = hip_status(launch_grad_in_bf16(dgu, (const uint16_t *)w->w1, offsets, tiles, n_tiles, max_tiles, p->H,
+                                            p->I, (uint16_t *)dx_perm, stream));
+    if (!st && dw1)
+        st = hip_status(launch_wgrad_bf16(dgu, 2 * p->I, (const uint16_t *)x_perm, p->H, offsets, order, p->E,
+                                          (uint16_t *)dw1, stream));
+    if (!st && dw2)
+        st = hip_status(launch_wgrad_bf16((const uint16_t *)dy_perm, p->H, h, p->I, offsets, order, p->E,
+                                          (uint16_t *)dw2, stream));
+    return st;
 }
 
 int moe_w4a8_dequant_table(uint8_t *out8, hipStream_t stream) {

@@ -86,6 +86,9 @@ WsLayout ws_layout(const moe_problem &p);
 hipError_t launch_route_topk(const float *logits, const uint8_t *slot_drop, int T, int E, int k, int32_t *topk_idx,
                              float *topk_w, hipStream_t s);
 
+hipError_t launch_route_topk_backward(const float *logits, const uint8_t *slot_drop, const float *dtopk_w, int T,
+                                      int E, int k, float *dlogits, hipStream_t s);
+
 hipError_t launch_tables(const int32_t *topk_idx, int T, int k, int E, int32_t *chunk_counts, int32_t *offsets,
                          int32_t *row_src, int32_t *slot_row, int bm, int by_expert, int32_t *tiles,
                          int32_t *n_tiles, hipStream_t s);
@@ -103,9 +106,10 @@ hipError_t launch_frontend_small(const float *logits, const uint8_t *slot_drop, 
                                  int32_t *row_src, int32_t *slot_row, int32_t *tiles, int32_t *n_tiles,
                                  hipStream_t s);
 
+// gu NULL, or [S][2I]: the pre-activations are stored too, in W1's stored row order
 hipError_t launch_gemm1_swiglu_bf16(const uint16_t *x_perm, const uint16_t *w1, const int32_t *offsets,
                                     const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
-                                    int glu_interleave, float clamp, uint16_t *h, hipStream_t s);
+                                    int glu_interleave, float clamp, uint16_t *h, uint16_t *gu, hipStream_t s);
 
 // GEMM1 + SwiGLU reading its activation rows from the token rows x [T][H] through row_src
 // (the gather fused into the tile loads); needs gather_fits(T, H)
@@ -125,6 +129,19 @@ hipError_t launch_gemm1_swiglu_gather_bf16(const uint16_t *x, const int32_t *row
 hipError_t launch_gemm2_bf16(const uint16_t *h, const uint16_t *w2, const int32_t *offsets, const int32_t *tiles,
                              const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *y_perm,
                              const int32_t *row_dst, hipStream_t s);
+
+// Backward pass.  grad_glu: dh = dy W2, then dgu [S][2I] (stored row order) from dh and the kept gu, and
+// h [S][I] again; grad_in: dx = dgu W1
+hipError_t launch_grad_glu_bf16(const uint16_t *dy, const uint16_t *w2, const uint16_t *gu, const int32_t *offsets,
+                                const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
+                                int glu_interleave, float clamp, uint16_t *dgu, uint16_t *h, hipStream_t s);
+hipError_t launch_grad_in_bf16(const uint16_t *dgu, const uint16_t *w1, const int32_t *offsets, const int32_t *tiles,
+                               const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *dx, hipStream_t s);
+// Weight gradient of every expert: dw[e][m][n] = sum over e's rows r of p[r][m] q[r][n]; p [S][M],
+// q [S][N], dw [E][M][N]; M and N multiples of 128.  order [E]: the experts, most rows first.
+hipError_t launch_expert_order(const int32_t *offsets, int E, int32_t *order, hipStream_t s);
+hipError_t launch_wgrad_bf16(const uint16_t *p, int M, const uint16_t *q, int N, const int32_t *offsets,
+                             const int32_t *order, int E, uint16_t *dw, hipStream_t s);
 
 // row_src NULL: x_perm / x_perm_scale are the expert-ordered rows; else x / x_scale token rows
 // read through row_src (the gather fused into GEMM1; needs gather_fits_fp8(T, H)).  row_dst as
