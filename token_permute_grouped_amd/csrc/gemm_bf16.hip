@@ -57,18 +57,12 @@
 // the way the FlashInfer split kernels fold dispatch into their first GEMM.  Each
 // 128-byte piece of a row is still one whole cache line, so the loads stay coalesced.
 //
-// Gradients.  dh = dy W2 and dx = dgu W1 are the same loop with the weights read as [K][N] rows: a
-// stage is then 64 weight rows of 256 columns, brought in by the same DMAs, and the weight fragments
-// come through the LDS's transposing reads (load_trans), so no transposed copy of the weights is made
-// (it would cost 4.3 + 8.6 GB of traffic on the skewed layer).  dh stays in fp32 through the gradient
-// of the SwiGLU, which is formed in the epilogue.
-//
 // Scheduling.  The device-side tile list gives the m-tiles (expert, first row);
 // tile_map assigns them to workgroups by band and XCD rectangle (below).
 // Workgroups past the tile count exit before any barrier.
 #include <type_traits>
 
-#include "gemm_trans.h"
+#include "gemm_common.h"
 
 namespace tpg {
 
@@ -97,21 +91,6 @@ constexpr int kBStagesSp = 4;
 static_assert(kBBaseSp + kBStagesSp * kBStage <= kBBase + kBStages * kBStage, "sparse layout fits the LDS");
 static_assert(kSpRows == kLRows, "a sparse stage is the first activation load of every thread");
 
-// Workgroup -> tile map.  Workgroup b runs on XCD b % 8.  Bands of tm.gm m-tiles take
-// tm.per_band workgroups each; a band is cut into 8 rectangles (xm rows of m-tiles x xn
-// columns of n-tiles, about 32 tiles each: one per CU of an XCD), and XCD x takes
-// rectangle x.  The 32 tiles an XCD runs at once then share ~8 activation slabs and ~4
-// weight slabs in its L2, and all XCDs stay on one band (a few experts) in the MALL.
-struct TileMap {
-    int xn, nc, gm, per_band;  // rectangle columns, n-tiles per column, band m-tiles, workgroups per band
-};
-__host__ __device__ inline TileMap tile_map(int nb_n) {
-    const int xn = nb_n >= 4 ? 4 : nb_n >= 2 ? 2 : 1;
-    const int nc = (nb_n + xn - 1) / xn;
-    const int rm = 32 / nc > 1 ? 32 / nc : 1;  // m-tiles per rectangle
-    return {xn, nc, (8 / xn) * rm, 8 * rm * nc};
-}
-
 __device__ __forceinline__ int slot(int r, int kc) { return kc ^ ((r & 7) ^ ((r >> 3) & 1)); }
 
 __device__ __forceinline__ float silu_mul(float g, float u, float clamp) {
@@ -125,28 +104,6 @@ __device__ __forceinline__ float silu_mul(float g, float u, float clamp) {
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return pack_bf16x2(a, b);
-}
-
-// Gradient of h = silu(g) u at the kept pre-activations: dg, du for dh, and h itself.  The clamp is
-// min(max(v, -c), c); its gradient is 0 outside [-c, c] and 1 on the border.
-__device__ __forceinline__ void glu_grad(float g0, float u0, float dh, float clamp, float &dg, float &du, float &h) {
-    float g = g0, u = u0;
-    if (clamp > 0.f) {
-        g = fminf(fmaxf(g, -clamp), clamp);
-        u = fminf(fmaxf(u, -clamp), clamp);
-    }
-    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g)), gs = g * s;
-    h = gs * u;
-    dg = dh * u * (s + gs * (1.0f - s));
-    du = dh * gs;
-    if (clamp > 0.f) {
-        if (fabsf(g0) > clamp) dg = 0.f;
-        if (fabsf(u0) > clamp) du = 0.f;
-    }
-}
-
-__device__ __forceinline__ u32x4 pack8(const float *v) {
-    return (u32x4){pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
 }
 
 // pattern with extra work: per group, X instructions of class `cls`, one DS read, MFMAs
@@ -164,13 +121,10 @@ __device__ __forceinline__ void interleave_x_ds_mfma() {
 
 }  // namespace
 
-// The products of the forward and of the backward pass that have the token rows on their rows.
 enum class Gemm {
     kGlu,      // GEMM1 + SwiGLU -> h
     kGluKeep,  // the same, with the pre-activations stored too
     kOut,      // GEMM2 -> y
-    kGradGlu,  // dy W2 = dh, then the gradient of the SwiGLU -> dgu, and h again from the kept gu
-    kGradIn,   // dgu W1 -> dx
 };
 
 template <Gemm kKind>
@@ -186,34 +140,13 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     int K, int N, int I, int il, float clamp,
     uint16_t *__restrict__ C, int ldc,     // [S][ldc]
     const int32_t *__restrict__ row_dst,   // NULL, or [S]: row r of the tile order is stored to row row_dst[r] of C
-    const uint16_t *__restrict__ gu_in,    // kGradGlu: [S][2I] kept pre-activations
-    uint16_t *__restrict__ gu_out) {       // kGluKeep: [S][2I] pre-activations; kGradGlu: their gradients
-    constexpr bool kSwiGLU = kKind == Gemm::kGlu || kKind == Gemm::kGluKeep;
-    // gradients: the weights are read as [E][K][N], their K the row index of the stored matrix
-    constexpr bool kTrans = kKind == Gemm::kGradGlu || kKind == Gemm::kGradIn;
+    uint16_t *__restrict__ gu) {           // kGluKeep: [S][2I], the pre-activations
+    constexpr bool kSwiGLU = kKind != Gemm::kOut;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kBBase + kBStages * kBStage];  // 160 KB
 
     // ---- tile of this workgroup: band of m-tiles, XCD rectangle within the band, tile within it
-    const int nb_n = (N + kBN - 1) / kBN;
-    const TileMap tm = tile_map(nb_n);
-    const int n_mt = n_tiles[0];
-    const int band = blockIdx.x / tm.per_band, p = blockIdx.x % tm.per_band;
-    const int first_m = band * tm.gm;
-    const int gm = min(tm.gm, n_mt - first_m);  // m-tiles in this band
-    const int xm = 8 / tm.xn;
-    const int ma = (gm + xm - 1) / xm;          // m-tiles per rectangle row
-    const int x = p & 7, q = p >> 3;            // XCD (blockIdx % 8) and position on it
-    const int mi = q / tm.nc, ni = q % tm.nc;
-    const int v = first_m + (x / tm.xn) * ma + mi;  // position in the interleaved m-tile order
-    const int nt = (x % tm.xn) * tm.nc + ni;
-    if (gm <= 0 || mi >= ma || v >= first_m + gm || nt >= nb_n) return;
-    // The list holds the full m-tiles, then one partial m-tile per expert.  A partial tile
-    // does little MFMA work for the weights it streams, so partial tiles are spread evenly
-    // through the order (position v is partial when floor(v P / n) steps) and their weight
-    // streaming overlaps the full tiles' MFMAs instead of forming a memory-bound tail.
-    const int n_part = n_mt - n_tiles[1];
-    const int cp = (int)((int64_t)v * n_part / n_mt), cp1 = (int)((int64_t)(v + 1) * n_part / n_mt);
-    const int mt = cp1 > cp ? n_tiles[1] + cp : v - cp;
+    int mt, nt;
+    if (!row_tile(blockIdx.x, (N + kBN - 1) / kBN, n_tiles, mt, nt)) return;
 
     const int e = tiles[2 * mt];
     const int row_begin = offsets[e] + tiles[2 * mt + 1];
@@ -262,13 +195,6 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     };
 #pragma unroll
     for (int i = 0; i < kOpsB; ++i) {
-        if constexpr (kTrans) {
-            // stage row r: 256 columns of weight row kt * 64 + r (512 bytes, two rows per op)
-            const int r = wave * (kBK / kWaves) + i * 2 + (lane >> 5);
-            const int c = nt * kBN + tchunk(r, lane & 31) * 8;
-            offB[i] = c < N ? (uint32_t)(r * N + c) * 2u : 0x80000000u;  // columns past N: not read
-            continue;
-        }
         const int r = wave * (kBN / kWaves) + i * 8 + (lane >> 3);  // tile weight row
         int wr;
         if (kSwiGLU) {
@@ -301,7 +227,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     auto dmaB = [&](int kt, int bstage, int i0, int n, int BB) {
         unsigned char *dst = lds + BB + bstage * kBStage + wave * (kBN / kWaves) * kRowBytes;
 #pragma unroll
-        for (int i = i0; i < i0 + n; ++i) dma16(rsB, offB[i], kTrans ? kt * (kBK * 2) * N : kt * kRowBytes, dst + i * 1024);
+        for (int i = i0; i < i0 + n; ++i) dma16(rsB, offB[i], kt * kRowBytes, dst + i * 1024);
     };
 
     f32x16 acc[2][4];
@@ -320,7 +246,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     auto mainloop = [&](auto nb_tag, auto sp_tag) {
         constexpr int NB = decltype(nb_tag)::value;
         constexpr bool kSp = decltype(sp_tag)::value;  // sparse tile: at most 64 live rows
-        constexpr int NR = (kTrans ? 4 : 2) + NB;  // fragment reads per K step
+        constexpr int NR = 2 + NB;  // fragment reads per K step
         constexpr int NM = 2 * NB;  // MFMAs per K step
         constexpr int NL = kSp ? 1 : kLoads;            // activation loads per thread and stage
         constexpr int AS = kSp ? kAStageSp : kAStage;
@@ -336,12 +262,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
                 const int kc = ks * 2 + fk;
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    if constexpr (kTrans) {
-                        fw[buf][a] = load_trans(lds + BB + bstage * kBStage, wn * 64 + a * 32, ks, lane);
-                    } else {
-                        const int r = wn * 64 + a * 32 + fr;
-                        fw[buf][a] = __builtin_bit_cast(bf16x8, sb[r * 8 + slot(r, kc)]);
-                    }
+                    const int r = wn * 64 + a * 32 + fr;
+                    fw[buf][a] = __builtin_bit_cast(bf16x8, sb[r * 8 + slot(r, kc)]);
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -496,54 +418,6 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     auto cofs = [](int r, int c) { return r * (kCols * 2) + ((c ^ (r & 15)) << 4); };
     const int half = lane >> 5;
     lds_barrier();  // every wave is done with the last stage's operands
-    if constexpr (kKind == Gemm::kGradGlu) {
-        // dh goes through LDS in fp32, 128 columns at a time (wave columns 0, 1, then 2, 3): a row of
-        // 32 chunks of 4 values, chunk c of row r at c ^ (r & 31).  A thread then takes 8 columns of a
-        // row: reads gate and up, writes both gradients and h, each 16 bytes.
-#pragma unroll 1
-        for (int p = 0; p < 2; ++p) {
-            if ((wn >> 1) == p) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int tr = wm * 128 + b * 32 + (lane & 31);
-#pragma unroll
-                    for (int a = 0; a < 2; ++a)
-#pragma unroll
-                        for (int g4 = 0; g4 < 4; ++g4) {
-                            const int c = (wn & 1) * 16 + a * 8 + g4 * 2 + half;
-                            *(f32x4 *)(lds + tr * 512 + ((c ^ (tr & 31)) << 4)) =
-                                (f32x4){acc[a][b][g4 * 4], acc[a][b][g4 * 4 + 1], acc[a][b][g4 * 4 + 2],
-                                        acc[a][b][g4 * 4 + 3]};
-                        }
-                }
-            }
-            lds_barrier();
-            const int c8 = tid & 15;                       // 8-column group of this thread
-            const int col = nt * kBN + p * 128 + c8 * 8;   // hidden column
-            const int gcol = il == 0 ? col : col / il * 2 * il + col % il, ucol = gcol + (il == 0 ? I : il);
-            if (col < N) {
-                for (int tr = tid >> 4; tr < rows; tr += kThreads / 16) {
-                    const int64_t r = row_begin + tr;
-                    const u32x4 gv = *(const u32x4 *)(gu_in + r * 2 * I + gcol);
-                    const u32x4 uv = *(const u32x4 *)(gu_in + r * 2 * I + ucol);
-                    const f32x4 d0 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2) ^ (tr & 31)) << 4));
-                    const f32x4 d1 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2 + 1) ^ (tr & 31)) << 4));
-                    float dg[8], du[8], hv[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float g = __uint_as_float(q & 1 ? gv[q >> 1] & 0xffff0000u : gv[q >> 1] << 16);
-                        const float u = __uint_as_float(q & 1 ? uv[q >> 1] & 0xffff0000u : uv[q >> 1] << 16);
-                        glu_grad(g, u, q < 4 ? d0[q & 3] : d1[q & 3], clamp, dg[q], du[q], hv[q]);
-                    }
-                    *(u32x4 *)(gu_out + r * 2 * I + gcol) = pack8(dg);
-                    *(u32x4 *)(gu_out + r * 2 * I + ucol) = pack8(du);
-                    *(u32x4 *)(C + r * ldc + col) = pack8(hv);
-                }
-            }
-            lds_barrier();
-        }
-        return;
-    }
     if constexpr (kKind == Gemm::kGluKeep) {
         // the pre-activations first, a 256-column bf16 tile in W1's stored row order: a contiguous
         // run of 256 (interleaved rows), or 128 gate and 128 up columns I apart
@@ -568,7 +442,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
 #pragma unroll 4
         for (int tr = wave * 2 + half; tr < kBM; tr += kWaves * 2)
             if (tr < rows)
-                *(u32x4 *)(gu_out + (int64_t)(row_begin + tr) * 2 * I + gc) = *(const u32x4 *)(lds + gofs(tr, tc));
+                *(u32x4 *)(gu + (int64_t)(row_begin + tr) * 2 * I + gc) = *(const u32x4 *)(lds + gofs(tr, tc));
         lds_barrier();
     }
 #pragma unroll
@@ -617,12 +491,12 @@ template <Gemm kKind>
 hipError_t launch(const uint16_t *A, const int32_t *row_src, int gather_k, int a_rows, const uint16_t *W,
                   const int32_t *offsets, const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int K,
                   int N, int I, int il, float clamp, uint16_t *C, int ldc, const int32_t *row_dst, hipStream_t s,
-                  const uint16_t *gu_in = nullptr, uint16_t *gu_out = nullptr) {
+                  uint16_t *gu = nullptr) {
     const int nb_n = (N + kBN - 1) / kBN;
     const TileMap tm = tile_map(nb_n);
     const int64_t blocks = (max_tiles + tm.gm - 1) / tm.gm * tm.per_band;
     hipLaunchKernelGGL(grouped_gemm_bf16_kernel<kKind>, dim3(blocks), dim3(kThreads), 0, s, A, row_src, gather_k,
-                       a_rows, W, offsets, tiles, n_tiles, K, N, I, il, clamp, C, ldc, row_dst, gu_in, gu_out);
+                       a_rows, W, offsets, tiles, n_tiles, K, N, I, il, clamp, C, ldc, row_dst, gu);
     return hipGetLastError();
 }
 }  // namespace
@@ -632,7 +506,7 @@ hipError_t launch_gemm1_swiglu_bf16(const uint16_t *x_perm, const uint16_t *w1, 
                                     int glu_interleave, float clamp, uint16_t *h, uint16_t *gu, hipStream_t s) {
     if (gu)
         return launch<Gemm::kGluKeep>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
-                                      glu_interleave, clamp, h, I, nullptr, s, nullptr, gu);
+                                      glu_interleave, clamp, h, I, nullptr, s, gu);
     return launch<Gemm::kGlu>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
                               glu_interleave, clamp, h, I, nullptr, s);
 }
@@ -651,19 +525,6 @@ hipError_t launch_gemm2_bf16(const uint16_t *h, const uint16_t *w2, const int32_
                              const int32_t *row_dst, hipStream_t s) {
     return launch<Gemm::kOut>(h, nullptr, 1, 0, w2, offsets, tiles, n_tiles, max_tiles, I, H, I, 0, 0.0f, y_perm, H,
                               row_dst, s);
-}
-
-hipError_t launch_grad_glu_bf16(const uint16_t *dy, const uint16_t *w2, const uint16_t *gu, const int32_t *offsets,
-                                const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
-                                int glu_interleave, float clamp, uint16_t *dgu, uint16_t *h, hipStream_t s) {
-    return launch<Gemm::kGradGlu>(dy, nullptr, 1, 0, w2, offsets, tiles, n_tiles, max_tiles, H, I, I, glu_interleave,
-                                  clamp, h, I, nullptr, s, gu, dgu);
-}
-
-hipError_t launch_grad_in_bf16(const uint16_t *dgu, const uint16_t *w1, const int32_t *offsets, const int32_t *tiles,
-                               const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *dx, hipStream_t s) {
-    return launch<Gemm::kGradIn>(dgu, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, 2 * I, H, I, 0, 0.0f, dx,
-                                 H, nullptr, s);
 }
 
 }  // namespace tpg

@@ -1,0 +1,82 @@
+// Building blocks shared by the bf16 GEMM kernels: buffer DMAs into LDS, their waits, the scheduling
+// pattern, the mapping of workgroups to token-row tiles.
+#pragma once
+#include "moe_internal.h"
+
+namespace tpg {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+// one 16-byte-per-lane DMA from a raw buffer straight into LDS (1 KB per wave, lane-linear)
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t soff, void *dst) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// LDS barrier without a global-memory fence: register loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// scheduling pattern: NR fragment reads (DS) spread evenly over M MFMAs
+template <int NR, int M, int I = 0>
+__device__ __forceinline__ void interleave_ds_mfma() {
+    if constexpr (I < NR) {
+        constexpr int m = (M * (I + 1)) / NR - (M * I) / NR;
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                       // DS read
+        if constexpr (m > 0) __builtin_amdgcn_sched_group_barrier(0x008, m, 0);  // MFMA
+        interleave_ds_mfma<NR, M, I + 1>();
+    }
+}
+
+// Workgroup -> tile map.  Workgroup b runs on XCD b % 8.  Bands of tm.gm m-tiles take
+// tm.per_band workgroups each; a band is cut into 8 rectangles (xm rows of m-tiles x xn
+// columns of n-tiles, about 32 tiles each: one per CU of an XCD), and XCD x takes
+// rectangle x.  The 32 tiles an XCD runs at once then share ~8 activation slabs and ~4
+// weight slabs in its L2, and all XCDs stay on one band (a few experts) in the MALL.
+struct TileMap {
+    int xn, nc, gm, per_band;  // rectangle columns, n-tiles per column, band m-tiles, workgroups per band
+};
+__host__ __device__ inline TileMap tile_map(int nb_n) {
+    const int xn = nb_n >= 4 ? 4 : nb_n >= 2 ? 2 : 1;
+    const int nc = (nb_n + xn - 1) / xn;
+    const int rm = 32 / nc > 1 ? 32 / nc : 1;  // m-tiles per rectangle
+    return {xn, nc, (8 / xn) * rm, 8 * rm * nc};
+}
+
+
+// (m-tile, n-tile) of workgroup `block`; false if it has none.  The list holds the full m-tiles, then one
+// partial m-tile per expert.  A partial tile does little MFMA work for the weights it streams, so
+// partial tiles are spread evenly through the order (position v is partial when floor(v P / n) steps) and
+// their weight streaming overlaps the full tiles' MFMAs instead of forming a memory-bound tail.
+__device__ __forceinline__ bool row_tile(int block, int nb_n, const int32_t *__restrict__ n_tiles, int &mt, int &nt) {
+    const TileMap tm = tile_map(nb_n);
+    const int n_mt = n_tiles[0];
+    const int band = block / tm.per_band, p = block % tm.per_band;
+    const int first_m = band * tm.gm;
+    const int gm = min(tm.gm, n_mt - first_m);  // m-tiles in this band
+    const int xm = 8 / tm.xn;
+    const int ma = (gm + xm - 1) / xm;          // m-tiles per rectangle row
+    const int x = p & 7, q = p >> 3;            // XCD (block % 8) and position on it
+    const int mi = q / tm.nc, ni = q % tm.nc;
+    const int v = first_m + (x / tm.xn) * ma + mi;  // position in the interleaved m-tile order
+    nt = (x % tm.xn) * tm.nc + ni;
+    if (gm <= 0 || mi >= ma || v >= first_m + gm || nt >= nb_n) return false;
+    const int n_part = n_mt - n_tiles[1];
+    const int cp = (int)((int64_t)v * n_part / n_mt), cp1 = (int)((int64_t)(v + 1) * n_part / n_mt);
+    mt = cp1 > cp ? n_tiles[1] + cp : v - cp;
+    return true;
+}
+
+}  // namespace
+
+}  // namespace tpg

@@ -1,0 +1,411 @@
+// The four products of the grouped FFN's backward pass in bf16 on CDNA4 matrix cores
+// (v_mfma_f32_32x32x16_bf16), for the rows r of every expert e:
+//
+//     dh  = dy W2_e        then dgu and h from dh and the kept gu      (GradGlu)    2 R H I flops
+//     dx  = dgu W1_e                                                  (GradIn)     4 R H I
+//     dW1_e = dgu^T x      dW2_e = dy^T h     (sums over e's rows)    (GradWeight) 4 and 2 R H I
+//
+// All of them are C[i][j] = sum_k P[i or k] Q[k][j]: Q has the sum's index on its rows (weights as they are
+// stored, or token rows), P has it along its rows (GradGlu, GradIn: token rows) or on them (GradWeight).  The
+// operands with k on their rows would need a transposed copy for plain fragment reads (17 GB of traffic
+// on the layer with T = 16384, H = 4096, I = 2048, E = 128, k = 8); here they go into LDS as they are and come out
+// through its transposing reads (load_trans).
+//
+// Tile and pipeline.  A workgroup of 8 waves owns a 256 x 256 output tile, 128 x 64 per wave (4 x 2 blocks of 32 x
+// 32), two waves per SIMD.  A stage is 32 k of both operands, 32 KB, in a ring of five: every operand goes
+// straight to LDS by 16-byte-per-lane DMAs, requested five stages ahead.  A stage's one barrier stands
+// before its second 16-k step: by then every wave has read the stage's fragments, so its slot takes the DMAs
+// of the stage five ahead, and the next stage's first fragments load under the step's MFMAs.  The DMAs of
+// stages past the end are issued too (out of bounds, so nothing is read), so that one wait count fits every stage.
+//
+// The DMAs are inline assembly: the compiler waits for every DMA it knows of (vmcnt(0)) before a
+// transposing LDS read, which drained the ring each stage (dW1 of the layer above 6.4 ms, GradIn 4.5 ms).
+// They have no register outputs; wait_vmcnt and the barriers order them.
+//
+// LDS layout of a stage.  k on the rows: a row is 256 columns of one k, 512 bytes, sixteen 32-byte segments,
+// segment s of row r at s ^ 2 (r & 3); the transposing reads of 32 lanes then touch 8 distinct segments, one
+// per bank group.  k along the rows: a row is 32 k, 64 bytes, four 16-byte chunks, chunk c of row r at c ^ ((r >>
+// 2) & 3), so that 16 rows' reads touch all 16 bank groups.  The DMA's lanes fetch the chunk their place holds.
+//
+// Ragged ends.  Rows past the tile's or the expert's last read as zero by the buffers' bounds (GradWeight
+// sets base and bound for every stage, which also keeps row offsets 64-bit).  Columns past the matrix's
+// width are computed from whatever follows in memory within the bounds and are not stored.  GradGlu and GradIn
+// skip the MFMAs of 32-row blocks without a live row.
+//
+// Work order.  GradGlu and GradIn take m-tiles from the tile list by tile_map, as the forward does.
+// GradWeight takes the experts largest first; 32 (or fewer) neighbouring tiles of one expert form a
+// rectangle that one XCD (block index mod 8) works on at once, sharing its row and column slabs in that L2.
+#include <type_traits>
+
+#include "gemm_common.h"
+
+namespace tpg {
+
+namespace {
+constexpr int kBM = kGemmBM, kBN = 256, kBK = 32;
+constexpr int kWaves = 8, kThreads = 64 * kWaves, kWaveN = 4;
+constexpr int kHalf = kBK * 512;             // 16 KB: one operand of a stage
+constexpr int kStage = 2 * kHalf;            // P, then Q
+constexpr int kStages = 5;
+constexpr int kOps = kHalf / 1024 / kWaves;  // DMAs per wave, stage and operand (2)
+static_assert(kBM * kBK * 2 == kHalf && kBN * 2 == 512, "both operand layouts fill the same 16 KB");
+
+enum class Grad { kGlu, kIn, kWeight };
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// raw buffer of `bytes` bytes from p (p, bytes wave-uniform)
+__device__ __forceinline__ i32x4 buffer(const void *p, int bytes) {
+    const uint64_t a = (uint64_t)p;
+    return (i32x4){__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                   __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xffff),
+                   __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// 16 bytes per lane from the buffer to LDS address dst + 16 lane.  (m0 is a reserved register, which nothing
+// else in these kernels uses, so it is not and may not be named as clobbered.)
+__device__ __forceinline__ void dma(i32x4 rsrc, uint32_t voff, int soff, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(dst), "v"(voff), "s"(rsrc), "s"(soff));
+}
+
+// k on the rows: the logical 16-byte chunk that chunk position p of row r holds
+__device__ __forceinline__ int tchunk(int r, int p) { return p ^ ((r & 3) << 2); }
+
+// MFMA fragment of 32 columns n0.. and the 16 k of step ks: lane l gets column n0 + (l & 31), k = 16 ks +
+// 8 (l >> 5) + 0..7, by two transposing reads of 4 k each.  In one, lane i of a group of 16 names 4
+// columns (i & 3) of row i >> 2 and gets column i of the 4 rows.
+__device__ __forceinline__ bf16x8 load_trans(const unsigned char *stage, int n0, int ks, int lane) {
+    const int r = (lane & 15) >> 2, seg = (n0 >> 4) + ((lane >> 4) & 1);
+    const unsigned char *p =
+        stage + (ks * 16 + (lane >> 5) * 8 + r) * 512 + ((seg ^ (2 * r)) << 5) + (lane & 3) * 8;
+    typedef __attribute__((address_space(3))) bf16x4 *lds_ptr;
+    const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)p);
+    const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(p + 4 * 512));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// k along the rows: the logical chunk that chunk position p of row r holds, and the fragment of rows r0..
+__device__ __forceinline__ int kchunk(int r, int p) { return p ^ ((r >> 2) & 3); }
+__device__ __forceinline__ bf16x8 load_rows(const unsigned char *stage, int r0, int ks, int lane) {
+    const int r = r0 + (lane & 31);
+    return *(const bf16x8 *)(stage + r * 64 + (kchunk(r, ks * 2 + (lane >> 5)) << 4));
+}
+
+// Gradient of h = silu(g) u at the kept pre-activations: dg, du for dh, and h itself.  The clamp is
+// min(max(v, -c), c); its gradient is 0 outside [-c, c] and 1 on the border.
+__device__ __forceinline__ void glu_grad(float g0, float u0, float dh, float clamp, float &dg, float &du, float &h) {
+    float g = g0, u = u0;
+    if (clamp > 0.f) {
+        g = fminf(fmaxf(g, -clamp), clamp);
+        u = fminf(fmaxf(u, -clamp), clamp);
+    }
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g)), gs = g * s;
+    h = gs * u;
+    dg = dh * u * (s + gs * (1.0f - s));
+    du = dh * gs;
+    if (clamp > 0.f) {
+        if (fabsf(g0) > clamp) dg = 0.f;
+        if (fabsf(u0) > clamp) du = 0.f;
+    }
+}
+
+__device__ __forceinline__ u32x4 pack8(const float *v) {
+    return (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+struct Rects {
+    int rm, rn, cols, per_expert;  // tiles of a rectangle, rectangles along n, rectangles of an expert
+};
+__host__ __device__ inline Rects rects(int M, int N) {
+    const int nb_m = (M + kBM - 1) / kBM, nb_n = (N + kBN - 1) / kBN;
+    const int rn = nb_n < 8 ? nb_n : 8, rm = nb_m < 32 / rn ? nb_m : 32 / rn;
+    const int cols = (nb_n + rn - 1) / rn;
+    return {rm, rn, cols, cols * ((nb_m + rm - 1) / rm)};
+}
+}  // namespace
+
+// order[rank] = expert, by descending row count (ties: lower expert first); one workgroup of 256
+__global__ __launch_bounds__(256) void expert_order_kernel(const int32_t *__restrict__ offsets, int E,
+                                                           int32_t *__restrict__ order) {
+    __shared__ int cnt[256];
+    const int e = threadIdx.x;
+    cnt[e] = e < E ? offsets[e + 1] - offsets[e] : -1;
+    __syncthreads();
+    if (e >= E) return;
+    int rank = 0;
+    for (int i = 0; i < E; ++i) rank += cnt[i] > cnt[e] || (cnt[i] == cnt[e] && i < e);
+    order[rank] = e;
+}
+
+struct GradArgs {
+    const uint16_t *P, *Q;   // kGlu: dy [S][H], W2 [E][H][I]; kIn: dgu [S][2I], W1 [E][2I][H];
+                             // kWeight: [S][M], [S][N] token rows
+    int M, N, K;             // kGlu, kIn: N columns of Q, K of both; kWeight: M and N columns
+    const int32_t *offsets;  // [E+1]
+    const int32_t *tiles, *n_tiles;  // kGlu, kIn: m-tiles
+    const int32_t *order;    // kWeight: experts, most rows first
+    int E;
+    uint16_t *C;             // kGlu: h [S][I]; kIn: dx [S][H]; kWeight: [E][M][N]
+    const uint16_t *gu;      // kGlu: kept pre-activations [S][2I]
+    uint16_t *dgu;           // kGlu: their gradients
+    int il;                  // kGlu: gate/up row interleave
+    float clamp;
+};
+
+template <Grad kKind>
+__global__ __launch_bounds__(kThreads, 1) void grouped_grad_bf16_kernel(GradArgs a) {
+    constexpr bool kW = kKind == Grad::kWeight;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];  // 160 KB
+    const int N = a.N;
+
+    // ---- tile of this workgroup: expert e, rows m0.. (of its token rows, or of its gradient), columns n0..
+    int e, m0, n0;
+    if constexpr (kW) {
+        const Rects rc = rects(a.M, N);
+        const int area = rc.rm * rc.rn;
+        const int q = blockIdx.x >> 3, rect = q / area * 8 + (blockIdx.x & 7), in = q % area;
+        if (rect >= a.E * rc.per_expert) return;
+        const int re = rect % rc.per_expert;
+        e = a.order[rect / rc.per_expert];
+        m0 = ((re / rc.cols) * rc.rm + in / rc.rn) * kBM;
+        n0 = ((re % rc.cols) * rc.rn + in % rc.rn) * kBN;
+        if (m0 >= a.M || n0 >= N) return;
+    } else {
+        int mt, nt;
+        if (!row_tile(blockIdx.x, (N + kBN - 1) / kBN, a.n_tiles, mt, nt)) return;
+        e = a.tiles[2 * mt];
+        m0 = a.tiles[2 * mt + 1];
+        n0 = nt * kBN;
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    const int64_t row0 = __builtin_amdgcn_readfirstlane(a.offsets[e]);
+    const int count = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - (int)row0;
+    const int live = kW ? min(kBM, a.M - m0) : min(kBM, count - m0);  // live rows of the output tile
+    const int nk = kW ? (count + kBK - 1) / kBK : a.K / kBK;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / kWaveN, wn = wave % kWaveN;
+    const int half = lane >> 5;
+
+    // ---- DMAs of a stage: byte offsets of this lane's 16 bytes
+    uint32_t offP[kOps], offQ[kOps];
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) {
+        const int r = wave * (kBK / kWaves) + i * 2 + half, c = tchunk(r, lane & 31) * 8;  // stage row, column
+        // GradGlu, GradIn: columns past N are not read (the last row's would lie behind the matrix)
+        offQ[i] = !kW && n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
+        if constexpr (kW) {
+            offP[i] = (uint32_t)(r * a.M + m0 + c) * 2u;
+        } else {
+            const int pr = wave * (kBM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
+            offP[i] = pr < live ? (uint32_t)(pr * a.K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
+        }
+    }
+    const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
+    auto request = [&](int kt, int slot) {
+        const uint32_t dst = lds0 + slot * kStage;
+        if constexpr (kW) {
+            const int left = __builtin_amdgcn_readfirstlane(max(0, min(kBK, count - kt * kBK)));
+            const int64_t r = row0 + (left > 0 ? (int64_t)kt * kBK : 0);
+            const i32x4 p = buffer(a.P + r * a.M, left * a.M * 2), q = buffer(a.Q + r * N, left * N * 2);
+#pragma unroll
+            for (int i = 0; i < kOps; ++i) {
+                dma(p, offP[i], 0, dst + i * 1024);
+                dma(q, offQ[i], 0, dst + kHalf + i * 1024);
+            }
+        } else {
+            const bool in = kt < nk;
+            const i32x4 p = buffer(a.P + (row0 + m0) * a.K, in ? live * a.K * 2 : 0);
+            const i32x4 q = buffer(a.Q + (int64_t)e * a.K * N, in ? a.K * N * 2 : 0);
+            const int sp = in ? kt * kBK * 2 : 0, sq = in ? kt * kBK * 2 * N : 0;
+#pragma unroll
+            for (int i = 0; i < kOps; ++i) {
+                dma(p, offP[i], sp, dst + i * 1024);
+                dma(q, offQ[i], sq, dst + kHalf + i * 1024);
+            }
+        }
+    };
+
+    f32x16 acc[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[x][b][v] = 0.f;
+
+    // NB: 32-row blocks of this wave with a live row
+    auto mainloop = [&](auto nb_tag) {
+        constexpr int NB = decltype(nb_tag)::value;
+        constexpr int NR = (kW ? 2 : 1) * NB + 4, NM = 2 * NB;  // LDS reads and MFMAs of a step
+        constexpr int G = 2 * kOps;                            // DMAs of a stage
+        bf16x8 fq[2][2], fp[2][NB > 0 ? NB : 1];
+        auto load = [&](int buf, int slot, int ks) {
+            if constexpr (NB > 0) {
+                const unsigned char *s = lds + slot * kStage;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) fq[buf][x] = load_trans(s + kHalf, wn * 64 + x * 32, ks, lane);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    fp[buf][b] = kW ? load_trans(s, wm * 128 + b * 32, ks, lane) : load_rows(s, wm * 128 + b * 32, ks, lane);
+            }
+        };
+        auto mfmas = [&](int buf) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    acc[x][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[buf][x], fp[buf][b], acc[x][b], 0, 0, 0);
+        };
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) request(s, s);
+        wait_vmcnt<(kStages - 1) * G>();
+        lds_barrier();
+        load(0, 0, 0);
+        int slot = 0;
+        for (int kt = 0; kt < nk; ++kt) {
+            load(1, slot, 1);
+            mfmas(0);
+            if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+            wait_vmcnt<(kStages - 2) * G>();  // stage kt+1 has landed; kt+2 .. kt+4 may be in flight
+            lds_barrier();
+            request(kt + kStages, slot);
+            slot = slot + 1 == kStages ? 0 : slot + 1;
+            load(0, slot, 0);
+            mfmas(1);
+            if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+        }
+        wait_vmcnt<0>();  // the LDS is written again below
+    };
+    switch (kW ? 4 : max(0, min(4, (live - wm * 128 + 31) >> 5))) {
+        case 4: mainloop(std::integral_constant<int, 4>{}); break;
+        case 3: if constexpr (!kW) mainloop(std::integral_constant<int, 3>{}); break;
+        case 2: if constexpr (!kW) mainloop(std::integral_constant<int, 2>{}); break;
+        case 1: if constexpr (!kW) mainloop(std::integral_constant<int, 1>{}); break;
+        default: if constexpr (!kW) mainloop(std::integral_constant<int, 0>{}); break;
+    }
+
+    // ---- epilogue: lane holds tile row wm 128 + b 32 + (lane & 31) and columns wn 64 + x 32 + 8 (v >> 2) +
+    //      4 (lane >> 5) + (v & 3).  The tile goes through LDS, so that whole rows are read and stored.
+    lds_barrier();
+    if constexpr (kKind == Grad::kGlu) {
+        // dh goes through LDS in fp32, 128 columns at a time (wave columns 0, 1, then 2, 3): a row of
+        // 32 chunks of 4 values, chunk c of row r at c ^ (r & 31).  A thread then takes 8 columns of a
+        // row: reads gate and up, writes both gradients and h, each 16 bytes.
+#pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+            if ((wn >> 1) == p) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int tr = wm * 128 + b * 32 + (lane & 31);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int g4 = 0; g4 < 4; ++g4) {
+                            const int c = (wn & 1) * 16 + x * 8 + g4 * 2 + half;
+                            *(f32x4 *)(lds + tr * 512 + ((c ^ (tr & 31)) << 4)) =
+                                (f32x4){acc[x][b][g4 * 4], acc[x][b][g4 * 4 + 1], acc[x][b][g4 * 4 + 2],
+                                        acc[x][b][g4 * 4 + 3]};
+                        }
+                }
+            }
+            lds_barrier();
+            const int c8 = tid & 15;                       // 8-column group of this thread
+            const int col = n0 + p * 128 + c8 * 8;         // hidden column
+            const int gcol = a.il == 0 ? col : col / a.il * 2 * a.il + col % a.il, ucol = gcol + (a.il == 0 ? N : a.il);
+            if (col < N) {
+                for (int tr = tid >> 4; tr < live; tr += kThreads / 16) {
+                    const int64_t r = row0 + m0 + tr;
+                    const u32x4 gv = *(const u32x4 *)(a.gu + r * 2 * N + gcol);
+                    const u32x4 uv = *(const u32x4 *)(a.gu + r * 2 * N + ucol);
+                    const f32x4 d0 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2) ^ (tr & 31)) << 4));
+                    const f32x4 d1 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2 + 1) ^ (tr & 31)) << 4));
+                    float dg[8], du[8], hv[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float g = __uint_as_float(q & 1 ? gv[q >> 1] & 0xffff0000u : gv[q >> 1] << 16);
+                        const float u = __uint_as_float(q & 1 ? uv[q >> 1] & 0xffff0000u : uv[q >> 1] << 16);
+                        glu_grad(g, u, q < 4 ? d0[q & 3] : d1[q & 3], a.clamp, dg[q], du[q], hv[q]);
+                    }
+                    *(u32x4 *)(a.dgu + r * 2 * N + gcol) = pack8(dg);
+                    *(u32x4 *)(a.dgu + r * 2 * N + ucol) = pack8(du);
+                    *(u32x4 *)(a.C + r * N + col) = pack8(hv);
+                }
+            }
+            lds_barrier();
+        }
+        return;
+    }
+    auto cofs = [](int r, int c) { return r * (kBN * 2) + ((c ^ (r & 15)) << 4); };
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const int tr = wm * 128 + b * 32 + (lane & 31);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int g4 = 0; g4 < 4; ++g4) {
+                u32x2 o;
+                o.x = pack_bf16x2(acc[x][b][g4 * 4 + 0], acc[x][b][g4 * 4 + 1]);
+                o.y = pack_bf16x2(acc[x][b][g4 * 4 + 2], acc[x][b][g4 * 4 + 3]);
+                *(u32x2 *)(lds + cofs(tr, wn * 8 + x * 4 + g4) + half * 8) = o;
+            }
+    }
+    lds_barrier();
+    const int c = n0 + (lane & 31) * 8;
+    if (c < N) {
+        uint16_t *out = a.C + ((kW ? (int64_t)e * a.M : row0) + m0) * N + c;
+#pragma unroll 4
+        for (int tr = wave * 2 + half; tr < kBM; tr += kWaves * 2)
+            if (tr < live) *(u32x4 *)(out + (int64_t)tr * N) = *(const u32x4 *)(lds + cofs(tr, lane & 31));
+    }
+}
+
+hipError_t launch_expert_order(const int32_t *offsets, int E, int32_t *order, hipStream_t s) {
+    hipLaunchKernelGGL(expert_order_kernel, dim3(1), dim3(256), 0, s, offsets, E, order);
+    return hipGetLastError();
+}
+
+namespace {
+template <Grad kKind>
+hipError_t launch_rows(const GradArgs &a, int64_t max_tiles, hipStream_t s) {
+    const TileMap tm = tile_map((a.N + kBN - 1) / kBN);
+    const int64_t blocks = (max_tiles + tm.gm - 1) / tm.gm * tm.per_band;
+    hipLaunchKernelGGL(grouped_grad_bf16_kernel<kKind>, dim3(blocks), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_grad_glu_bf16(const uint16_t *dy, const uint16_t *w2, const uint16_t *gu, const int32_t *offsets,
+                                const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
+                                int glu_interleave, float clamp, uint16_t *dgu, uint16_t *h, hipStream_t s) {
+    GradArgs a = {};
+    a.P = dy, a.Q = w2, a.N = I, a.K = H, a.offsets = offsets, a.tiles = tiles, a.n_tiles = n_tiles;
+    a.C = h, a.gu = gu, a.dgu = dgu, a.il = glu_interleave, a.clamp = clamp;
+    return launch_rows<Grad::kGlu>(a, max_tiles, s);
+}
+
+hipError_t launch_grad_in_bf16(const uint16_t *dgu, const uint16_t *w1, const int32_t *offsets, const int32_t *tiles,
+                               const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *dx, hipStream_t s) {
+    GradArgs a = {};
+    a.P = dgu, a.Q = w1, a.N = H, a.K = 2 * I, a.offsets = offsets, a.tiles = tiles, a.n_tiles = n_tiles, a.C = dx;
+    return launch_rows<Grad::kIn>(a, max_tiles, s);
+}
+
+hipError_t launch_grad_weight_bf16(const uint16_t *p, int M, const uint16_t *q, int N, const int32_t *offsets,
+                                   const int32_t *order, int E, uint16_t *dw, hipStream_t s) {
+    const Rects rc = rects(M, N);
+    const int64_t blocks = ((int64_t)E * rc.per_expert + 7) / 8 * 8 * rc.rm * rc.rn;
+    GradArgs a = {};
+    a.P = p, a.Q = q, a.M = M, a.N = N, a.offsets = offsets, a.order = order, a.E = E, a.C = dw;
+    hipLaunchKernelGGL(grouped_grad_bf16_kernel<Grad::kWeight>, dim3(blocks), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace tpg

@@ -600,11 +600,11 @@ int moe_grouped_ffn_backward(const void *dy_perm, const void *x_perm, const void
         st = hip_status(launch_grad_in_bf16(dgu, (const uint16_t *)w->w1, offsets, tiles, n_tiles, max_tiles, p->H,
                                             p->I, (uint16_t *)dx_perm, stream));
     if (!st && dw1)
-        st = hip_status(launch_wgrad_bf16(dgu, 2 * p->I, (const uint16_t *)x_perm, p->H, offsets, order, p->E,
-                                          (uint16_t *)dw1, stream));
+        st = hip_status(launch_grad_weight_bf16(dgu, 2 * p->I, (const uint16_t *)x_perm, p->H, offsets, order, p->E,
+                                                (uint16_t *)dw1, stream));
     if (!st && dw2)
-        st = hip_status(launch_wgrad_bf16((const uint16_t *)dy_perm, p->H, h, p->I, offsets, order, p->E,
-                                          (uint16_t *)dw2, stream));
+        st = hip_status(launch_grad_weight_bf16((const uint16_t *)dy_perm, p->H, h, p->I, offsets, order, p->E,
+                                                (uint16_t *)dw2, stream));
     return st;
 }
 

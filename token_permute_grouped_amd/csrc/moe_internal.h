@@ -140,8 +140,8 @@ hipError_t launch_grad_in_bf16(const uint16_t *dgu, const uint16_t *w1, const in
 // Weight gradient of every expert: dw[e][m][n] = sum over e's rows r of p[r][m] q[r][n]; p [S][M],
 // q [S][N], dw [E][M][N]; M and N multiples of 128.  order [E]: the experts, most rows first.
 hipError_t launch_expert_order(const int32_t *offsets, int E, int32_t *order, hipStream_t s);
-hipError_t launch_wgrad_bf16(const uint16_t *p, int M, const uint16_t *q, int N, const int32_t *offsets,
-                             const int32_t *order, int E, uint16_t *dw, hipStream_t s);
+hipError_t launch_grad_weight_bf16(const uint16_t *p, int M, const uint16_t *q, int N, const int32_t *offsets,
+                                   const int32_t *order, int E, uint16_t *dw, hipStream_t s);
 
 // row_src NULL: x_perm / x_perm_scale are the expert-ordered rows; else x / x_scale token rows
 // read through row_src (the gather fused into GEMM1; needs gather_fits_fp8(T, H)).  row_dst as
