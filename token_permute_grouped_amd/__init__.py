@@ -61,19 +61,21 @@ class Weights(ctypes.Structure):
 
 class Norm(ctypes.Structure):
     _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+    weight_tensor = None  # what make_norm was given
 
 
 class Residual(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("scale", ctypes.c_float), ("gate", ctypes.c_void_p),
                 ("gate_kind", ctypes.c_int32)]
+    x_tensor = gate_tensor = None  # what make_residual was given
 
 
-_lib = None
+_lib = _torch = None
 
 
 def load() -> ctypes.CDLL:
     """Load libtpg_moe.so (built in-tree by token_permute_grouped_amd._build)."""
-    global _lib
+    global _lib, _torch
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -81,7 +83,8 @@ def load() -> ctypes.CDLL:
                           "(or __graft_entry__.build()); there is no fallback path")
     # torch first: it carries the process's HIP runtime (same SONAME as the one this library links), so
     # torch's streams and allocations and this library's launches share one runtime instance
-    import torch  # noqa: F401
+    import torch
+    _torch = torch
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     PP = ctypes.POINTER(Problem)
@@ -138,8 +141,8 @@ def _nbytes(t):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without its stream object (2.8 us of the host's time a call)
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -258,7 +261,7 @@ def moe_w4a8_dequant_table(out8, stream=None):
 def make_norm(weight, eps) -> Norm:
     """weight: bf16 [H] or None (ones)"""
     n = Norm(_ptr(weight), eps)
-    n.tensors = lambda p: [(weight, 2 * p.H)]
+    n.weight_tensor = weight
     return n
 
 
@@ -267,39 +270,61 @@ def make_residual(x, scale=1.0, gate=None, gate_kind=MOE_GATE_NONE) -> Residual:
     if gate_kind == MOE_GATE_NONE:
         gate = None
     r = Residual(_ptr(x), scale, _ptr(gate), gate_kind)
-    r.tensors = lambda p: [(x, 2 * p.T * p.H), (gate, 4 * (p.H if gate_kind == MOE_GATE_CHANNEL else p.T))]
+    r.x_tensor, r.gate_tensor = x, gate
     return r
 
 
-def _call(fn: str, p: Problem, stream, args, sizes):
-    """Calls `fn` with args (tensors become addresses, descriptors pointers) and the stream.  sizes:
-    (tensor, bytes it has to hold)."""
-    device = None
-    for a in args:
-        if hasattr(a, "tensors"):
-            sizes += a.tensors(p)
+def _bad_tensor(fn, t, n):
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: a tensor of shape {tuple(t.shape)} is not contiguous")
+    raise ValueError(f"{fn}: a tensor of shape {tuple(t.shape)} holds {t.nbytes} bytes, the problem needs {n}")
+
+
+def _pointers(fn: str, T: int, sizes):
+    """(device index, addresses) of sizes = ((tensor, address or None; bytes), ...); the index is None
+    without tensors"""
+    dev, ptrs = None, []
     for t, n in sizes:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
+            ptrs.append(t)
             continue
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: a tensor of shape {tuple(t.shape)} is not contiguous")
-        if _nbytes(t) < n:
-            raise ValueError(f"{fn}: a tensor of shape {tuple(t.shape)} holds {_nbytes(t)} bytes, the problem needs {n}")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{fn}: tensors on {device} and {t.device}")
-    call = getattr(load(), fn)
-    args = [ctypes.byref(a) if isinstance(a, ctypes.Structure) else _ptr(a) for a in args]
-    if device is None or device.type != "cuda":
-        if device is not None and p.T > 0:
-            raise ValueError(f"{fn}: tensors on {device}, not on a GPU")
-        return _check(fn, call(*args, _stream(stream)))
-    import torch
-    if device.index == torch.cuda.current_device():
-        return _check(fn, call(*args, _stream(stream)))
-    with torch.cuda.device(device):
-        return _check(fn, call(*args, _stream(stream)))
+        if not t.is_contiguous() or t.nbytes < n:
+            _bad_tensor(fn, t, n)
+        d = t.get_device()
+        if d != dev:
+            if dev is not None:
+                raise ValueError(f"{fn}: tensors on different devices")
+            dev = d
+        ptrs.append(t.data_ptr())
+    if dev == -1 and T > 0:
+        raise ValueError(f"{fn}: tensors that are not on a GPU")
+    return dev, ptrs
+
+
+def _call(fn: str, dev, stream, *args):
+    f = getattr(_lib, fn)
+    if dev is None or dev < 0 or dev == _torch.cuda.current_device():
+        st = f(*args, _stream(stream))
+    else:
+        with _torch.cuda.device(dev):
+            st = f(*args, _stream(stream))
+    if st != MOE_OK:
+        _check(fn, st)
+
+
+def _ref(descriptor):
+    return None if descriptor is None else ctypes.byref(descriptor)
+
+
+def _weight_of(norm):
+    return None if norm is None else norm.weight_tensor
+
+
+def _tensors_of(residual, T, H):
+    if residual is None:
+        return (None, 0), (None, 0)
+    return ((residual.x_tensor, 2 * T * H),
+            (residual.gate_tensor, 4 * (H if residual.gate_kind == MOE_GATE_CHANNEL else T)))
 
 
 def _ws_bytes(ws, ws_bytes):
@@ -308,67 +333,98 @@ def _ws_bytes(ws, ws_bytes):
 
 def moe_prenorm(x, norm, problem: Problem, xn=None, xn8=None, xn_scale=None, stream=None):
     """norm: make_norm(...) or None"""
-    n = problem.T * problem.H
-    _call("moe_prenorm", problem, stream, [x, norm, problem, xn, xn8, xn_scale],
-          [(x, 2 * n), (xn, 2 * n), (xn8, n), (xn_scale, n // 32)])
+    load()
+    T, H = problem.T, problem.H
+    n = T * H
+    dev, (x, xn, xn8, xn_scale, _) = _pointers("moe_prenorm", T, (
+        (x, 2 * n), (xn, 2 * n), (xn8, n), (xn_scale, n // 32), (_weight_of(norm), 2 * H)))
+    _call("moe_prenorm", dev, stream, x, _ref(norm), ctypes.byref(problem), xn, xn8, xn_scale)
 
 
 def moe_prenorm_backward(dx_perm, slot_row, dxn, dres, x, norm, problem: Problem, dx, dweight=None, ws=None,
                          ws_bytes=None, stream=None):
-    n, S = problem.T * problem.H, problem.T * problem.k
-    _call("moe_prenorm_backward", problem, stream,
-          [dx_perm, slot_row, dxn, dres, x, norm, problem, dx, dweight, ws, _ws_bytes(ws, ws_bytes)],
-          [(dx_perm, 2 * S * problem.H), (slot_row, 4 * S), (dxn, 2 * n), (dres, 2 * n), (x, 2 * n), (dx, 2 * n),
-           (dweight, 4 * problem.H), (ws, 0)])
+    load()
+    T, H = problem.T, problem.H
+    n, S = 2 * T * H, T * problem.k
+    ws_bytes = _ws_bytes(ws, ws_bytes)
+    dev, (dx_perm, slot_row, dxn, dres, x, dx, dweight, ws, _) = _pointers("moe_prenorm_backward", T, (
+        (dx_perm, 2 * S * H), (slot_row, 4 * S), (dxn, n), (dres, n), (x, n), (dx, n), (dweight, 4 * H), (ws, 0),
+        (_weight_of(norm), 2 * H)))
+    _call("moe_prenorm_backward", dev, stream, dx_perm, slot_row, dxn, dres, x, _ref(norm), ctypes.byref(problem), dx,
+          dweight, ws, ws_bytes)
 
 
 def moe_combine_norm(y_perm, slot_row, topk_w, norm, residual, problem: Problem, out, stream=None):
     """residual: make_residual(...) or None"""
-    n, S = problem.T * problem.H, problem.T * problem.k
-    _call("moe_combine_norm", problem, stream, [y_perm, slot_row, topk_w, norm, residual, problem, out],
-          [(y_perm, 2 * S * problem.H), (slot_row, 4 * S), (topk_w, 4 * S), (out, 2 * n)])
+    load()
+    T, H = problem.T, problem.H
+    S = T * problem.k
+    dev, (y_perm, slot_row, topk_w, out, _, _, _) = _pointers("moe_combine_norm", T, (
+        (y_perm, 2 * S * H), (slot_row, 4 * S), (topk_w, 4 * S), (out, 2 * T * H), (_weight_of(norm), 2 * H),
+        *_tensors_of(residual, T, H)))
+    _call("moe_combine_norm", dev, stream, y_perm, slot_row, topk_w, _ref(norm), _ref(residual),
+          ctypes.byref(problem), out)
 
 
 def moe_combine_norm_backward(dout, y_perm, slot_row, topk_w, norm, residual, problem: Problem, dy_perm, dtopk_w=None,
                               dresidual=None, dweight=None, dgate=None, ws=None, ws_bytes=None, stream=None):
-    n, S = problem.T * problem.H, problem.T * problem.k
-    token_gate = residual is not None and residual.gate_kind == MOE_GATE_TOKEN
-    _call("moe_combine_norm_backward", problem, stream,
-          [dout, y_perm, slot_row, topk_w, norm, residual, problem, dy_perm, dtopk_w, dresidual, dweight, dgate, ws,
-           _ws_bytes(ws, ws_bytes)],
-          [(dout, 2 * n), (y_perm, 2 * S * problem.H), (slot_row, 4 * S), (topk_w, 4 * S), (dy_perm, 2 * S * problem.H),
-           (dtopk_w, 4 * S), (dresidual, 2 * n), (dweight, 4 * problem.H),
-           (dgate, 4 * (problem.T if token_gate else problem.H)), (ws, 0)])
+    load()
+    T, H = problem.T, problem.H
+    n, S = 2 * T * H, T * problem.k
+    ws_bytes = _ws_bytes(ws, ws_bytes)
+    gate_n = 4 * (T if residual is not None and residual.gate_kind == MOE_GATE_TOKEN else H)
+    dev, (dout, y_perm, slot_row, topk_w, dy_perm, dtopk_w, dresidual, dweight, dgate, ws, _, _, _) = _pointers(
+        "moe_combine_norm_backward", T, (
+            (dout, n), (y_perm, 2 * S * H), (slot_row, 4 * S), (topk_w, 4 * S), (dy_perm, 2 * S * H), (dtopk_w, 4 * S),
+            (dresidual, n), (dweight, 4 * H), (dgate, gate_n), (ws, 0), (_weight_of(norm), 2 * H),
+            *_tensors_of(residual, T, H)))
+    _call("moe_combine_norm_backward", dev, stream, dout, y_perm, slot_row, topk_w, _ref(norm), _ref(residual),
+          ctypes.byref(problem), dy_perm, dtopk_w, dresidual, dweight, dgate, ws, ws_bytes)
 
 
 def moe_forward_norm(logits, slot_drop, x, x_scale, weights: Weights, norm, residual, problem: Problem, out, ws,
                      ws_bytes=None, stream=None):
-    T, H, S = problem.T, problem.H, problem.T * problem.k
+    load()
+    T, H = problem.T, problem.H
     bf16 = problem.prec == MOE_PREC_BF16
-    _call("moe_forward_norm", problem, stream,
-          [logits, slot_drop, x, x_scale, weights, norm, residual, problem, out, ws, _ws_bytes(ws, ws_bytes)],
-          [(logits, 4 * T * problem.E), (slot_drop, S), (x, (2 if bf16 else 1) * T * H),
-           (x_scale, 0 if bf16 else T * H // 32), (out, 2 * T * H), (ws, 0)])
+    ws_bytes = _ws_bytes(ws, ws_bytes)
+    dev, (logits, slot_drop, x, x_scale, out, ws, _, _, _) = _pointers("moe_forward_norm", T, (
+        (logits, 4 * T * problem.E), (slot_drop, T * problem.k), (x, (2 if bf16 else 1) * T * H),
+        (x_scale, 0 if bf16 else T * H // 32), (out, 2 * T * H), (ws, 0), (_weight_of(norm), 2 * H),
+        *_tensors_of(residual, T, H)))
+    _call("moe_forward_norm", dev, stream, logits, slot_drop, x, x_scale, _ref(weights), _ref(norm), _ref(residual),
+          ctypes.byref(problem), out, ws, ws_bytes)
 
 
 def moe_route_topk_backward(logits, slot_drop, dtopk_w, problem: Problem, dlogits, stream=None):
-    n, S = 4 * problem.T * problem.E, problem.T * problem.k
-    _call("moe_route_topk_backward", problem, stream, [logits, slot_drop, dtopk_w, problem, dlogits],
-          [(logits, n), (slot_drop, S), (dtopk_w, 4 * S), (dlogits, n)])
+    load()
+    T = problem.T
+    n, S = 4 * T * problem.E, T * problem.k
+    dev, (logits, slot_drop, dtopk_w, dlogits) = _pointers("moe_route_topk_backward", T, (
+        (logits, n), (slot_drop, S), (dtopk_w, 4 * S), (dlogits, n)))
+    _call("moe_route_topk_backward", dev, stream, logits, slot_drop, dtopk_w, ctypes.byref(problem), dlogits)
 
 
 def moe_grouped_ffn_train(x_perm, offsets, weights: Weights, problem: Problem, gu, y_perm, ws, ws_bytes=None,
                           stream=None):
-    n = 2 * problem.T * problem.k * problem.H
-    _call("moe_grouped_ffn_train", problem, stream,
-          [x_perm, offsets, weights, problem, gu, y_perm, ws, _ws_bytes(ws, ws_bytes)],
-          [(x_perm, n), (offsets, 4 * problem.E + 4), (gu, 4 * problem.T * problem.k * problem.I), (y_perm, n), (ws, 0)])
+    load()
+    S = problem.T * problem.k
+    n = 2 * S * problem.H
+    ws_bytes = _ws_bytes(ws, ws_bytes)
+    dev, (x_perm, offsets, gu, y_perm, ws) = _pointers("moe_grouped_ffn_train", problem.T, (
+        (x_perm, n), (offsets, 4 * problem.E + 4), (gu, 4 * S * problem.I), (y_perm, n), (ws, 0)))
+    _call("moe_grouped_ffn_train", dev, stream, x_perm, offsets, _ref(weights), ctypes.byref(problem), gu, y_perm, ws,
+          ws_bytes)
 
 
 def moe_grouped_ffn_backward(dy_perm, x_perm, gu, offsets, weights: Weights, problem: Problem, dx_perm=None, dw1=None,
                              dw2=None, ws=None, ws_bytes=None, stream=None):
-    n, w = 2 * problem.T * problem.k * problem.H, 2 * problem.E * problem.H * problem.I
-    _call("moe_grouped_ffn_backward", problem, stream,
-          [dy_perm, x_perm, gu, offsets, weights, problem, dx_perm, dw1, dw2, ws, _ws_bytes(ws, ws_bytes)],
-          [(dy_perm, n), (x_perm, n), (gu, 4 * problem.T * problem.k * problem.I), (offsets, 4 * problem.E + 4),
-           (dx_perm, n), (dw1, 2 * w), (dw2, w), (ws, 0)])
+    load()
+    S, H, I = problem.T * problem.k, problem.H, problem.I
+    n, w = 2 * S * H, 2 * problem.E * H * I
+    ws_bytes = _ws_bytes(ws, ws_bytes)
+    dev, (dy_perm, x_perm, gu, offsets, dx_perm, dw1, dw2, ws) = _pointers("moe_grouped_ffn_backward", problem.T, (
+        (dy_perm, n), (x_perm, n), (gu, 4 * S * I), (offsets, 4 * problem.E + 4), (dx_perm, n), (dw1, 2 * w), (dw2, w),
+        (ws, 0)))
+    _call("moe_grouped_ffn_backward", dev, stream, dy_perm, x_perm, gu, offsets, _ref(weights), ctypes.byref(problem),
+          dx_perm, dw1, dw2, ws, ws_bytes)

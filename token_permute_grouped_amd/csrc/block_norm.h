@@ -38,7 +38,7 @@ hipError_t launch_combine_norm(const uint16_t *y, const int32_t *slot_row, const
                                const moe_residual *residual, const moe_problem &p, bool slot_order, uint16_t *out,
                                hipStream_t s);
 
-// part: 2 * norm_partials(p) * H floats (unused without dweight and a channel gate's dgate)
+// part: norm_partials(p) * H floats (unused without dweight and a channel gate's dgate)
 hipError_t launch_combine_norm_backward(const void *dout, const void *y, const int32_t *slot_row, const float *topk_w,
                                         const moe_norm *norm, const moe_residual *residual, const moe_problem &p,
                                         void *dy, float *dtopk_w, void *dresidual, float *dweight, float *dgate,

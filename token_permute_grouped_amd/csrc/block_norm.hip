@@ -48,14 +48,45 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float *f) {
     }
 }
 
-__device__ __forceinline__ float wave_sum(float x) {
+// unpack8 of a value that was unpacked before: not to be kept unpacked in between (8 registers for 4)
+__device__ __forceinline__ void unpack_again(uint4 &v, float *f) {
+    asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+    unpack8(v, f);
+}
+
+// Lane sums.  A swap of half waves (or of odd with even rows of 16 lanes) between two values' registers and an
+// addition halve the values and the lanes at once.
+__device__ __forceinline__ float row_sum(float x) {
     using namespace wave;
     x += __uint_as_float(dpp<kQuadSwap1, 0xf>(__float_as_uint(x), 0u));
     x += __uint_as_float(dpp<kQuadSwap2, 0xf>(__float_as_uint(x), 0u));
     x += __uint_as_float(dpp<kRowHalfMirror, 0xf>(__float_as_uint(x), 0u));
-    x += __uint_as_float(dpp<kRowMirror, 0xf>(__float_as_uint(x), 0u));  // every lane: the sum of its row of 16
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
+    return x + __uint_as_float(dpp<kRowMirror, 0xf>(__float_as_uint(x), 0u));
+}
+__device__ __forceinline__ float fold32(float a, float b) {  // lanes 0..31: a over both halves; 32..63: b
+    const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(v[0]) + __uint_as_float(v[1]);
+}
+__device__ __forceinline__ float fold16(float a, float b) {  // even rows: a over the pair of rows; odd rows: b
+    const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(v[0]) + __uint_as_float(v[1]);
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    x = row_sum(x);
+    x = fold16(x, x);
+    return fold32(x, x);
+}
+// four values: the lanes of row i get value i's sum
+__device__ __forceinline__ float wave_sum4(const float (&v)[4]) {
+    return row_sum(fold16(fold32(v[0], v[2]), fold32(v[1], v[3])));
+}
+// the same for sixteen: the lanes of row i get values 4 i .. 4 i + 3
+__device__ __forceinline__ void wave_sum16(const float (&v)[16], float (&z)[4]) {
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = fold32(v[i], v[8 + i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = row_sum(fold16(u[i], u[4 + i]));
 }
 
 // Sums of N values over the workgroup, in every thread, in an order that depends on its size
@@ -79,11 +110,34 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *red) {
     }
 }
 
-// acc = fp32 fma chain over a token's live slots in ascending j of (w ? w[j] : 1) * row slot_row[j]
+// rows of token t's first eight slots (-1: none), wave-uniform
+struct Slots8 {
+    int32_t row[8];
+};
+__device__ __forceinline__ Slots8 load_slots8(const int32_t *slot_row, int64_t t, int k) {
+    Slots8 s;
+    const int32_t *slots = slot_row + t * k;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const int32_t r = slots[min(q, k - 1)];
+        s.row[q] = q < k ? r : -1;
+    }
+    return s;
+}
+// chunk c of those rows, 0 where there is none
+__device__ __forceinline__ void load_rows8(const uint4 *rows, const Slots8 &s, int row_vec, int c, uint4 (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        v[q] = make_uint4(0, 0, 0, 0);
+        if (s.row[q] >= 0) v[q] = load_once(rows + (int64_t)s.row[q] * row_vec + c);
+    }
+}
+
+// acc = fp32 fma chain over a token's live slots j >= first in ascending j of (w ? w[j] : 1) * row slot_row[j]
 // (or row j of the slot order); eight rows' loads are issued before any arithmetic
-__device__ __forceinline__ void slot_sum(const uint4 *rows, const int32_t *slots, const float *w, int64_t t, int k,
-                                         int row_vec, bool slot_order, int c, float *acc) {
-    for (int j0 = 0; j0 < k; j0 += 8) {
+__device__ __forceinline__ void slot_sum(const uint4 *rows, const int32_t *slots, const float *w, int64_t t, int first,
+                                         int k, int row_vec, bool slot_order, int c, float *acc) {
+    for (int j0 = first; j0 < k; j0 += 8) {
         uint4 v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -100,14 +154,13 @@ __device__ __forceinline__ void slot_sum(const uint4 *rows, const int32_t *slots
     }
 }
 
-__device__ __forceinline__ void weight8(const uint4 *w, int c, float *f) {
-    if (w) {
-        unpack8(w[c], f);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] = 1.0f;
-    }
+// eight bf16 weights of chunk c, or ones
+__device__ __forceinline__ uint4 load_weight(const uint4 *w, int c) {
+    if (w) return w[c];
+    constexpr uint32_t kOnes = 0x3f803f80;
+    return make_uint4(kOnes, kOnes, kOnes, kOnes);
 }
+__device__ __forceinline__ void weight8(const uint4 *w, int c, float *f) { unpack8(load_weight(w, c), f); }
 
 __device__ __forceinline__ void gate8(const float *gate, int kind, int64_t t, int c, float *f) {
     if (kind == MOE_GATE_CHANNEL) {
@@ -118,6 +171,17 @@ __device__ __forceinline__ void gate8(const float *gate, int kind, int64_t t, in
         const float g = kind == MOE_GATE_TOKEN ? gate[t] : 1.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) f[q] = g;
+    }
+}
+
+// the norm's weight times a channel gate (1 where there is none)
+__device__ __forceinline__ void channel_factor(const NormArgs &n, const ResidualArgs &res, int c, float *f) {
+    weight8(n.weight, c, f);
+    if (res.gate_kind == MOE_GATE_CHANNEL) {
+        float g[8];
+        gate8(res.gate, MOE_GATE_CHANNEL, 0, c, g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] *= g[q];
     }
 }
 
@@ -144,10 +208,12 @@ __global__ __launch_bounds__(1024) void prenorm_kernel(const uint4 *x, NormArgs 
     if (t >= T) return;
     const int nt = blockDim.x;
     float v[NC][8];
+    uint4 wv[NC];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * nt;
+        wv[i] = load_weight(n.weight, c < row_vec ? c : 0);
         if (c < row_vec) {
             unpack8(x[t * row_vec + c], v[i]);
 #pragma unroll
@@ -165,7 +231,7 @@ __global__ __launch_bounds__(1024) void prenorm_kernel(const uint4 *x, NormArgs 
         if (c >= row_vec) break;
         if (n.on) {
             float w[8];
-            weight8(n.weight, c, w);
+            unpack8(wv[i], w);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * r * w[q];
         }
@@ -190,6 +256,11 @@ __global__ __launch_bounds__(1024) void prenorm_kernel(const uint4 *x, NormArgs 
     }
 }
 
+// What one chunk of a token's gradient is made of: up to eight of its rows, and the three token rows.
+struct BackwardRows {
+    uint4 row[8], dxn, dres, x;
+};
+
 template <int NC>
 __global__ __launch_bounds__(1024) void prenorm_backward_kernel(const uint4 *dx_perm, const int32_t *slot_row,
                                                                 const uint4 *dxn, const uint4 *dres, const uint4 *x,
@@ -198,28 +269,68 @@ __global__ __launch_bounds__(1024) void prenorm_backward_kernel(const uint4 *dx_
     __shared__ float red[2][kMaxWaves * 2];
     const int nt = blockDim.x;
     float dw[NC][8] = {};
+    uint4 wv[NC];
+    BackwardRows raw;
+    Slots8 slots = {};
+    auto request_slots = [&](int64_t t) {
+        if (dx_perm && t < T) slots = load_slots8(slot_row, t, k);
+    };
+    auto request = [&](int64_t t, int c) {
+        if (dx_perm) load_rows8(dx_perm, slots, row_vec, c, raw.row);
+        raw.dxn = raw.dres = raw.x = make_uint4(0, 0, 0, 0);
+        if (dxn) raw.dxn = dxn[t * row_vec + c];
+        if (dres) raw.dres = dres[t * row_vec + c];
+        if (n.on) raw.x = x[t * row_vec + c];
+    };
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * nt;
+        wv[i] = load_weight(n.weight, c < row_vec ? c : 0);
+    }
+    // a thread behind the row's end takes its first chunk along and stores nothing
+    const int c1 = threadIdx.x < row_vec ? threadIdx.x : 0;
+    request_slots(blockIdx.x);
+    if constexpr (NC == 1) {
+        request(blockIdx.x, c1);
+        request_slots((int64_t)blockIdx.x + gridDim.x);
+    }
     int flip = 0;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
-        float dn[NC][8], v[NC][8];
+        float dn[NC][8];
+        uint4 xv[NC], dv[NC];
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = threadIdx.x + i * nt;
-            if (c >= row_vec) break;
 #pragma unroll
             for (int q = 0; q < 8; ++q) dn[i][q] = 0.f;
-            if (dx_perm) slot_sum(dx_perm, slot_row + t * k, nullptr, t, k, row_vec, false, c, dn[i]);
-            if (dxn) combine_fma8(dn[i], 1.0f, dxn[t * row_vec + c]);
+            if (c >= row_vec) continue;
+            if constexpr (NC > 1) request(t, c);
+            if (dx_perm) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) combine_fma8(dn[i], 1.0f, raw.row[q]);
+                if (k > 8) slot_sum(dx_perm, slot_row + t * k, nullptr, t, 8, k, row_vec, false, c, dn[i]);
+            }
+            combine_fma8(dn[i], 1.0f, raw.dxn);
+            dv[i] = raw.dres;
+            xv[i] = raw.x;
             if (n.on) {
-                float w[8];
-                unpack8(x[t * row_vec + c], v[i]);
-                weight8(n.weight, c, w);
+                float w[8], v[8];
+                unpack8(xv[i], v);
+                unpack8(wv[i], w);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    s[0] = fmaf(v[i][q], v[i][q], s[0]);
-                    s[1] = fmaf(dn[i][q] * w[q], v[i][q], s[1]);
+                    s[0] = fmaf(v[q], v[q], s[0]);
+                    s[1] = fmaf(dn[i][q] * w[q], v[q], s[1]);
                 }
             }
+        }
+        if constexpr (NC == 1) {
+            // the next token's rows are on their way during this one's reduction and stores
+            if (t + gridDim.x < T) request(t + gridDim.x, c1);
+            request_slots(t + 2 * (int64_t)gridDim.x);
+        } else {
+            request_slots(t + gridDim.x);
         }
         float r = 1.0f, coef = 0.0f;
         if (n.on) {
@@ -231,15 +342,16 @@ __global__ __launch_bounds__(1024) void prenorm_backward_kernel(const uint4 *dx_
         for (int i = 0; i < NC; ++i) {
             const int c = threadIdx.x + i * nt;
             if (c >= row_vec) break;
-            float o[8] = {};
-            if (dres) unpack8(dres[t * row_vec + c], o);
+            float o[8];
+            unpack8(dv[i], o);
             if (n.on) {
-                float w[8];
-                weight8(n.weight, c, w);
+                float w[8], v[8];
+                unpack8(xv[i], v);
+                unpack8(wv[i], w);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    dw[i][q] = fmaf(dn[i][q], v[i][q] * r, dw[i][q]);
-                    o[q] += r * (dn[i][q] * w[q]) - v[i][q] * coef;
+                    dw[i][q] = fmaf(dn[i][q], v[q] * r, dw[i][q]);
+                    o[q] += r * (dn[i][q] * w[q]) - v[q] * coef;
                 }
             } else {
 #pragma unroll
@@ -269,14 +381,17 @@ __global__ __launch_bounds__(1024) void combine_norm_kernel(const uint4 *__restr
     if (t >= T) return;
     const int nt = blockDim.x;
     float v[NC][8];
+    uint4 wv[NC], rv[NC];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * nt;
         if (c >= row_vec) break;
+        wv[i] = load_weight(n.weight, c);
+        rv[i] = res.x ? res.x[t * row_vec + c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[i][q] = 0.f;
-        slot_sum(y, slot_row + t * k, topk_w + t * k, t, k, row_vec, slot_order, c, v[i]);
+        slot_sum(y, slot_row + t * k, topk_w + t * k, t, 0, k, row_vec, slot_order, c, v[i]);
 #pragma unroll
         for (int q = 0; q < 8; ++q) s[0] = fmaf(v[i][q], v[i][q], s[0]);
     }
@@ -289,80 +404,73 @@ __global__ __launch_bounds__(1024) void combine_norm_kernel(const uint4 *__restr
     for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * nt;
         if (c >= row_vec) break;
-        float g[8], w[8];
+        float g[8], w[8], o[8];
         gate8(res.gate, res.gate_kind, t, c, g);
         if (n.on) {
-            weight8(n.weight, c, w);
+            unpack8(wv[i], w);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * r * w[q];
         }
-        float o[8];
-        if (res.x) {
-            unpack8(res.x[t * row_vec + c], o);
+        unpack8(rv[i], o);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = fmaf(res.scale, o[q], g[q] * v[i][q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = g[q] * v[i][q];
-        }
+        for (int q = 0; q < 8; ++q) o[q] = fmaf(res.scale, o[q], g[q] * v[i][q]);
         out[t * row_vec + c] = combine_pack8(o);
     }
 }
 
+// Per channel both the norm's weight and a channel gate are one factor f = gate weight (1 where there is none), so that
+// b = token_gate f dout.  One sum over tokens then serves both gradients: with a = sum_t token_gate dout c r,
+// dweight = gate a and dgate = weight a (formed by column_sum), and a token gate's gradient is r (f dout . c).
 template <int NC>
 __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(
     const uint4 *dout, const uint4 *y, const int32_t *__restrict__ slot_row, const float *__restrict__ topk_w,
     NormArgs n, ResidualArgs res, int T, int k, int row_vec, uint4 *dy, float *__restrict__ dtopk_w, uint4 *dresidual,
-    float *__restrict__ dgate_token, float *__restrict__ part_w, float *__restrict__ part_g) {
-    __shared__ float red[kMaxWaves * 3], dots[2][kMaxWaves * 8];
+    float *__restrict__ dgate_token, float *__restrict__ part) {
+    __shared__ float red[kMaxWaves * 2], dots[2][kMaxWaves * 8];
     const int nt = blockDim.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = nt >> 6;
-    float dw[NC][8] = {}, dg[NC][8] = {};
+    float a[NC][8] = {};
     int flip = 0;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         const int32_t *slots = slot_row + t * k;
         const float *tw = topk_w + t * k;
+        const float tok = res.gate_kind == MOE_GATE_TOKEN ? res.gate[t] : 1.0f;
         float c_[NC][8], d_[NC][8];  // the combined row, and dout
-        float s[3] = {0.f, 0.f, 0.f};
+        float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = threadIdx.x + i * nt;
             if (c >= row_vec) break;
 #pragma unroll
             for (int q = 0; q < 8; ++q) c_[i][q] = 0.f;
-            slot_sum(y, slots, tw, t, k, row_vec, false, c, c_[i]);
+            slot_sum(y, slots, tw, t, 0, k, row_vec, false, c, c_[i]);
             unpack8(dout[t * row_vec + c], d_[i]);
-            float w[8], g[8];
-            weight8(n.weight, c, w);
-            gate8(res.gate, res.gate_kind, t, c, g);
+            float f[8];
+            channel_factor(n, res, c, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float dwc = d_[i][q] * w[q] * c_[i][q];
                 s[0] = fmaf(c_[i][q], c_[i][q], s[0]);
-                s[1] = fmaf(g[q], dwc, s[1]);
-                s[2] += dwc;
+                s[1] = fmaf(f[q] * d_[i][q], c_[i][q], s[1]);
             }
         }
-        block_sum<3>(s, red);
+        block_sum<2>(s, red);
         float r = 1.0f, coef = 0.0f;
         if (n.on) {
             r = rsqrtf(s[0] * n.inv_h + n.eps);
-            coef = s[1] * n.inv_h * r * r * r;
+            coef = tok * s[1] * n.inv_h * r * r * r;
         }
-        if (dgate_token && threadIdx.x == 0) dgate_token[t] = s[2] * r;
+        if (dgate_token && threadIdx.x == 0) dgate_token[t] = s[1] * r;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = threadIdx.x + i * nt;
             if (c >= row_vec) break;
-            float w[8], g[8], o[8];
-            weight8(n.weight, c, w);
-            gate8(res.gate, res.gate_kind, t, c, g);
+            float f[8], o[8];
+            channel_factor(n, res, c, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float ch = c_[i][q] * r;
-                dw[i][q] = fmaf(d_[i][q] * g[q], ch, dw[i][q]);
-                dg[i][q] = fmaf(d_[i][q] * w[q], ch, dg[i][q]);
+                const float dt = tok * d_[i][q];
+                a[i][q] = fmaf(dt, c_[i][q] * r, a[i][q]);
                 o[q] = d_[i][q] * res.scale;
-                d_[i][q] = r * (d_[i][q] * g[q] * w[q]) - c_[i][q] * coef;  // dc
+                d_[i][q] = r * (dt * f[q]) - c_[i][q] * coef;  // dc
             }
             if (dresidual) dresidual[t * row_vec + c] = combine_pack8(o);
         }
@@ -376,7 +484,8 @@ __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const int32_t row = j0 + q < k ? slots[j0 + q] : -1;
-                    v[q] = row >= 0 && dtopk_w ? y[(int64_t)row * row_vec + c] : make_uint4(0, 0, 0, 0);
+                    v[q] = make_uint4(0, 0, 0, 0);
+                    if (row >= 0 && dtopk_w) v[q] = y[(int64_t)row * row_vec + c];
                 }
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -411,19 +520,131 @@ __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * nt;
-        if (c >= row_vec) break;
-        if (part_w) store_partial8(part_w + (int64_t)blockIdx.x * row_vec * 8, c, dw[i]);
-        if (part_g) store_partial8(part_g + (int64_t)blockIdx.x * row_vec * 8, c, dg[i]);
+        if (part && c < row_vec) store_partial8(part + (int64_t)blockIdx.x * row_vec * 8, c, a[i]);
     }
 }
 
-// out[h] = sum over the G partial rows, in a fixed order: 32 columns and 32 row groups per workgroup
+// The same for rows of one chunk per thread and k <= 8, which is what fits in registers: the token's rows are
+// read once.  dw_j = dc . y_j = r (b . y_j) - r^3 mean(b c) (c . y_j) needs no second look at them once r is
+// known, so all 2 + 2 k sums go through one reduction, and the next token's rows are requested before it.
+__global__ __launch_bounds__(1024) void combine_norm_backward8_kernel(
+    const uint4 *dout, const uint4 *y, const int32_t *__restrict__ slot_row, const float *__restrict__ topk_w,
+    NormArgs n, ResidualArgs res, int T, int k, int row_vec, uint4 *dy, float *__restrict__ dtopk_w, uint4 *dresidual,
+    float *__restrict__ dgate_token, float *__restrict__ part) {
+    __shared__ float red[2][kMaxWaves][16 + 4];  // f dout . y_j, c . y_j, then |c|^2, f dout . c
+    const int nt = blockDim.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = nt >> 6;
+    const bool in = threadIdx.x < row_vec;
+    const int c = in ? threadIdx.x : 0;  // a thread behind the row's end takes chunk 0 along, times 0
+    float a[8] = {}, f[8];
+    uint4 raw[8], draw;
+    Slots8 next;
+    auto request = [&](int64_t t) {
+        load_rows8(y, next, row_vec, c, raw);
+        draw = dout[t * row_vec + c];
+    };
+    next = load_slots8(slot_row, blockIdx.x, k);
+    request(blockIdx.x);
+    channel_factor(n, res, c, f);
+    int flip = 0;
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
+        const Slots8 cur = next;
+        if (t + gridDim.x < T) next = load_slots8(slot_row, t + gridDim.x, k);
+        float tw[8], tok = 1.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) tw[q] = topk_w[t * k + min(q, k - 1)];
+        if (res.gate_kind == MOE_GATE_TOKEN) tok = res.gate[t];
+        float cc[8] = {}, sums[4] = {0.f, 0.f, 0.f, 0.f}, dots[16];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (cur.row[q] >= 0) combine_fma8(cc, tw[q], raw[q]);
+        uint4 d4 = draw;
+        float d[8];
+        unpack8(d4, d);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            d[q] *= f[q];
+            sums[0] = fmaf(cc[q], cc[q], sums[0]);
+            sums[1] = fmaf(d[q], cc[q], sums[1]);
+        }
+        if (dtopk_w) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float v[8], dy1 = 0.f, cy = 0.f;
+                unpack_again(raw[q], v);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    dy1 = fmaf(d[z], v[z], dy1);
+                    cy = fmaf(cc[z], v[z], cy);
+                }
+                dots[q] = in ? dy1 : 0.f;
+                dots[8 + q] = in ? cy : 0.f;
+            }
+        }
+        // the next token's rows are on their way during the reduction and the stores
+        if (t + gridDim.x < T) request(t + gridDim.x);
+        if (!in) sums[0] = sums[1] = 0.f;
+        const float s1 = wave_sum4(sums);
+        if ((lane & 15) == 0) red[flip][wv][16 + (lane >> 4)] = s1;
+        if (dtopk_w) {
+            float z[4];
+            wave_sum16(dots, z);
+            if ((lane & 15) == 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) red[flip][wv][(lane >> 4) * 4 + i] = z[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            sums[i] = red[flip][0][16 + i];
+            for (int v = 1; v < nw; ++v) sums[i] += red[flip][v][16 + i];
+        }
+        float r = 1.0f, coef = 0.0f;
+        if (n.on) {
+            r = rsqrtf(sums[0] * n.inv_h + n.eps);
+            coef = tok * sums[1] * n.inv_h * r * r * r;
+        }
+        if (dtopk_w && threadIdx.x < k) {
+            float sd = 0.f, sc = 0.f;
+            for (int v = 0; v < nw; ++v) {
+                sd += red[flip][v][threadIdx.x];
+                sc += red[flip][v][8 + threadIdx.x];
+            }
+            dtopk_w[t * k + threadIdx.x] = slot_row[t * k + threadIdx.x] >= 0 ? r * tok * sd - coef * sc : 0.f;
+        }
+        if (dgate_token && threadIdx.x == 0) dgate_token[t] = sums[1] * r;
+        if (!in) continue;
+        float o[8];
+        unpack_again(d4, d);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            o[q] = d[q] * res.scale;
+            d[q] *= tok;
+            a[q] = fmaf(d[q], cc[q] * r, a[q]);
+            d[q] = r * (d[q] * f[q]) - cc[q] * coef;  // dc
+        }
+        if (dresidual) dresidual[t * row_vec + c] = combine_pack8(o);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (cur.row[q] < 0) continue;
+#pragma unroll
+            for (int z = 0; z < 8; ++z) o[z] = tw[q] * d[z];
+            dy[(int64_t)cur.row[q] * row_vec + c] = combine_pack8(o);
+        }
+    }
+    if (in && part) store_partial8(part + (int64_t)blockIdx.x * row_vec * 8, c, a);
+}
+
+// Sums a[h] over the G partial rows, in a fixed order: 32 columns and 32 row groups per workgroup.  out = a, times the
+// channel gate if there is one; dgate = a times the norm's weight (each if not NULL).
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restrict__ part, int G, int H,
-                                                          float *__restrict__ out) {
+                                                          const float *__restrict__ gate,
+                                                          const uint16_t *__restrict__ weight,
+                                                          float *__restrict__ out, float *__restrict__ dgate) {
     __shared__ float red[32][33];
     const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int h = blockIdx.x * 32 + col;  // H is a multiple of 128
     float s = 0.f;
+#pragma unroll 8
     for (int g = grp; g < G; g += 32) s += part[(int64_t)g * H + h];
     red[grp][col] = s;
     __syncthreads();
@@ -431,7 +652,8 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restric
         float a = 0.f;
 #pragma unroll
         for (int g = 0; g < 32; ++g) a += red[g][col];
-        out[h] = a;
+        if (out) out[h] = gate ? a * gate[h] : a;
+        if (dgate) dgate[h] = weight ? a * bf16_to_f32(weight[h]) : a;
     }
 }
 
@@ -504,7 +726,8 @@ hipError_t launch_prenorm_backward(const void *dx_perm, const int32_t *slot_row,
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !dweight) return e;
-    hipLaunchKernelGGL(column_sum_kernel, dim3(p.H / 32), dim3(1024), 0, s, part, G, p.H, dweight);
+    hipLaunchKernelGGL(column_sum_kernel, dim3(p.H / 32), dim3(1024), 0, s, part, G, p.H, (const float *)nullptr,
+                       (const uint16_t *)nullptr, dweight, (float *)nullptr);
     return hipGetLastError();
 }
 
@@ -526,24 +749,24 @@ hipError_t launch_combine_norm_backward(const void *dout, const void *y, const i
                                         float *part, hipStream_t s) {
     const RowShape rs = row_shape(p.H);
     const int G = norm_partials(p);
-    const bool channel = dgate && residual->gate_kind == MOE_GATE_CHANNEL;
-    float *part_w = dweight ? part : nullptr, *part_g = channel ? part + (size_t)G * p.H : nullptr;
-    with_chunks(rs.chunks, [&](auto nc) {
-        hipLaunchKernelGGL(combine_norm_backward_kernel<decltype(nc)::value>, dim3(G), dim3(rs.threads), 0, s,
-                           (const uint4 *)dout, (const uint4 *)y, slot_row, topk_w, norm_args(norm, p.H),
-                           residual_args(residual), p.T, p.k, p.H / 8, (uint4 *)dy, dtopk_w, (uint4 *)dresidual,
-                           channel ? nullptr : dgate, part_w, part_g);
-    });
+    const bool channel = residual && residual->gate_kind == MOE_GATE_CHANNEL;
+    const bool sums = dweight || (dgate && channel);
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(G), dim3(rs.threads), 0, s, (const uint4 *)dout, (const uint4 *)y, slot_row,
+                           topk_w, norm_args(norm, p.H), residual_args(residual), p.T, p.k, p.H / 8, (uint4 *)dy,
+                           dtopk_w, (uint4 *)dresidual, channel ? nullptr : dgate, sums ? part : nullptr);
+    };
+    if (rs.chunks == 1 && p.k <= 8)
+        run(combine_norm_backward8_kernel);
+    else
+        with_chunks(rs.chunks, [&](auto nc) { run(combine_norm_backward_kernel<decltype(nc)::value>); });
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && dweight) {
-        hipLaunchKernelGGL(column_sum_kernel, dim3(p.H / 32), dim3(1024), 0, s, part_w, G, p.H, dweight);
-        e = hipGetLastError();
-    }
-    if (e == hipSuccess && channel) {
-        hipLaunchKernelGGL(column_sum_kernel, dim3(p.H / 32), dim3(1024), 0, s, part_g, G, p.H, dgate);
-        e = hipGetLastError();
-    }
-    return e;
+    if (e != hipSuccess || !sums) return e;
+    hipLaunchKernelGGL(column_sum_kernel, dim3(p.H / 32), dim3(1024), 0, s, part, G, p.H,
+                       channel ? residual->gate : (const float *)nullptr,
+                       norm ? (const uint16_t *)norm->weight : (const uint16_t *)nullptr, dweight,
+                       channel ? dgate : (float *)nullptr);
+    return hipGetLastError();
 }
 
 }  // namespace tpg

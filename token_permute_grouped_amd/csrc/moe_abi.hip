@@ -337,7 +337,7 @@ size_t moe_call_workspace_bytes(const moe_problem *p, int which) {
         case MOE_WS_FORWARD: return L.forward_end;
         case MOE_WS_FFN_BACKWARD: return p->prec == MOE_PREC_BF16 ? backward_layout(*p).end : 0;
         case MOE_WS_PRENORM_BACKWARD: return partial_bytes(*p);
-        case MOE_WS_COMBINE_NORM_BACKWARD: return 2 * partial_bytes(*p);
+        case MOE_WS_COMBINE_NORM_BACKWARD: return partial_bytes(*p);
         default: return 0;
     }
 }
@@ -542,7 +542,7 @@ int moe_combine_norm_backward(const void *dout, const void *y_perm, const int32_
     const bool partials = dweight || (dgate && gate_kind == MOE_GATE_CHANNEL);
     if (partials && !ws) return MOE_ERR_NULL;
     if ((st = check_aligned(dout, y_perm, dy_perm, dresidual, ws))) return st;
-    if (partials && ws_bytes < 2 * partial_bytes(*p)) return MOE_ERR_WORKSPACE;
+    if (partials && ws_bytes < partial_bytes(*p)) return MOE_ERR_WORKSPACE;
     return hip_status(launch_combine_norm_backward(dout, y_perm, slot_row, topk_w, norm, residual, *p, dy_perm, dtopk_w,
                                                    dresidual, dweight, dgate, (float *)ws, stream));
 }

@@ -19,62 +19,95 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const float *__restrict
 // Gradient of the router.  With the chosen experts' weights w_j = exp(l_j) / sum_i exp(l_i) and the
 // gradients d_j that reached them (0 for a dropped slot),
 //     dlogits[chosen expert j] = w_j (d_j - sum_i w_i d_i),   0 for the other experts.
-// The chosen experts are found again from the logits (route_row's k rounds: E floats are read either
-// way, and a dropped slot's id is not in topk_idx), with sum_j exp(l_j - l_max) and sum_j exp(l_j -
-// l_max) d_j formed on the way; the lane that holds a winner keeps its exp and d.  One pass: reads T E
-// + T k, writes T E floats.
-template <int V>
-__device__ __forceinline__ void route_row_backward(const float *__restrict__ logits,
-                                                   const uint8_t *__restrict__ slot_drop,
-                                                   const float *__restrict__ dtopk_w, int64_t t, bool valid, int E,
-                                                   int k, int i, float *__restrict__ dlogits) {
+// The chosen experts are found again from the logits (E floats are read either way, and a dropped slot's id is not
+// in topk_idx): each of k rounds takes the row's largest key out and gives it the round's number, its slot.  One
+// pass: reads T E + T k, writes T E floats; the rounds' vector instructions bound it.  So a round first takes every
+// key equal to the maximum, without looking for the lowest expert id; only if that took more than k experts
+// (equal logits among the chosen) the wave starts over with the ids compared.  Up to 16 slots, lane i fetches slot
+// i's d before the rounds, and a winner's lane takes it from there.  T = 16384, E = 128, k = 8: 9.8-12.2 us with
+// route_row's rounds (ids, exp and d in each).
+// V: experts per lane (16 V >= E).  kWide: k > 16, d is loaded after the rounds.
+template <int V, bool kIds>
+__device__ __forceinline__ void choose(const float *__restrict__ l, int E, int k, int i, int (&slot)[V], float &lmax) {
     using namespace route_detail;
-    const float *l = logits + t * E;
     uint32_t key[V];
-    float ex[V], d[V];
 #pragma unroll
     for (int q = 0; q < V; ++q) {
         const int e = i + 16 * q;
         key[q] = e < E ? logit_key(l[e]) : 0u;
-        ex[q] = 0.0f;
-        d[q] = 0.0f;
+        slot[q] = -1;
     }
-    float lmax = 0.0f, z = 0.0f, zd = 0.0f;
     for (int j = 0; j < k; ++j) {
-        uint32_t bk = 0u;
-        int bq = 0;
+        uint32_t m = key[0];
 #pragma unroll
-        for (int q = 0; q < V; ++q)
-            if (key[q] > bk) {
-                bk = key[q];
-                bq = q;
-            }
-        const uint32_t m = row_max(bk);
-        const int win = (int)row_min(bk == m ? (uint32_t)(i + 16 * bq) : ~0u);
-        const float lj = key_logit(m);
-        if (j == 0) lmax = lj;
-        const float exj = expf(lj - lmax);
-        const int64_t s = t * k + j;
-        const float dj = slot_drop != nullptr && slot_drop[s] != 0 ? 0.0f : dtopk_w[s];
-        z += exj;
-        zd = fmaf(exj, dj, zd);
-        if ((win & 15) == i) {
+        for (int q = 1; q < V; ++q) m = max(m, key[q]);
+        m = row_max(m);
+        if (j == 0) lmax = key_logit(m);
+        uint32_t win = 0u;
+        if constexpr (kIds) {
+            win = ~0u;
 #pragma unroll
-            for (int q = 0; q < V; ++q)
-                if (q == (win >> 4)) {
-                    key[q] = 0u;
-                    ex[q] = exj;
-                    d[q] = dj;
-                }
+            for (int q = 0; q < V; ++q) win = min(win, key[q] == m ? (uint32_t)(i + 16 * q) : ~0u);
+            win = row_min(win);
+        }
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            const bool taken = kIds ? (uint32_t)(i + 16 * q) == win : key[q] == m && m != 0u;
+            slot[q] = taken ? j : slot[q];
+            key[q] = taken ? 0u : key[q];
         }
     }
-    if (!valid) return;
-    const float mean = zd / z;
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ T row_fold(T x, F add) {  // over the 16 lanes of a row, in every lane
+    using namespace wave;
+    x = add(x, __builtin_bit_cast(T, dpp<kQuadSwap1, 0xf>(__builtin_bit_cast(uint32_t, x), 0u)));
+    x = add(x, __builtin_bit_cast(T, dpp<kQuadSwap2, 0xf>(__builtin_bit_cast(uint32_t, x), 0u)));
+    x = add(x, __builtin_bit_cast(T, dpp<kRowHalfMirror, 0xf>(__builtin_bit_cast(uint32_t, x), 0u)));
+    return add(x, __builtin_bit_cast(T, dpp<kRowMirror, 0xf>(__builtin_bit_cast(uint32_t, x), 0u)));
+}
+
+template <int V, bool kWide>
+__device__ __forceinline__ void route_row_backward(const float *__restrict__ logits,
+                                                   const uint8_t *__restrict__ slot_drop,
+                                                   const float *__restrict__ dtopk_w, int64_t t, bool valid, int E,
+                                                   int k, int lane, float *__restrict__ dlogits) {
+    const int i = lane & 15;
+    const float *l = logits + t * E;
+    auto slot_grad = [&](int j) {
+        const int64_t s = t * k + j;
+        return slot_drop != nullptr && slot_drop[s] != 0 ? 0.0f : dtopk_w[s];
+    };
+    const float mine = !kWide && i < k ? slot_grad(i) : 0.0f;
+    int slot[V], taken = 0;
+    float lmax = 0.0f;
+    choose<V, false>(l, E, k, i, slot, lmax);
+#pragma unroll
+    for (int q = 0; q < V; ++q) taken += slot[q] >= 0;
+    taken = row_fold(taken, [](int a, int b) { return a + b; });
+    if (__any(taken != k)) choose<V, true>(l, E, k, i, slot, lmax);
+    float ex[V], d[V], z = 0.0f, zd = 0.0f;
 #pragma unroll
     for (int q = 0; q < V; ++q) {
         const int e = i + 16 * q;
-        // a taken expert's key is 0, every other's is not
-        if (e < E) dlogits[t * E + e] = key[q] == 0u ? ex[q] / z * (d[q] - mean) : 0.0f;
+        ex[q] = slot[q] >= 0 ? expf(l[min(e, E - 1)] - lmax) : 0.0f;
+        if constexpr (kWide)
+            d[q] = slot[q] >= 0 ? slot_grad(slot[q]) : 0.0f;
+        else
+            d[q] = __shfl(mine, (lane & 48) | max(slot[q], 0));
+        z += ex[q];
+        if (slot[q] >= 0) zd = fmaf(ex[q], d[q], zd);
+    }
+    const auto plus = [](float a, float b) { return a + b; };
+    z = row_fold(z, plus);
+    zd = row_fold(zd, plus);
+    if (!valid) return;
+    const float mean = zd / z, rz = 1.0f / z;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+        const int e = i + 16 * q;
+        if (e < E) dlogits[t * E + e] = slot[q] >= 0 ? ex[q] * rz * (d[q] - mean) : 0.0f;
     }
 }
 
@@ -89,7 +122,11 @@ __global__ __launch_bounds__(256) void route_topk_backward_kernel(const float *_
     const int64_t t0 = ((int64_t)blockIdx.y * kRouteGridX + blockIdx.x) * 16 + (threadIdx.x >> 6) * 4;
     if (t0 >= T) return;
     const int64_t t = t0 + (lane >> 4);
-    route_row_backward<V>(logits, slot_drop, dtopk_w, t < T ? t : T - 1, t < T, E, k, lane & 15, dlogits);
+    const int64_t tv = t < T ? t : T - 1;
+    if (k <= 16)
+        route_row_backward<V, false>(logits, slot_drop, dtopk_w, tv, t < T, E, k, lane, dlogits);
+    else
+        route_row_backward<V, true>(logits, slot_drop, dtopk_w, tv, t < T, E, k, lane, dlogits);
 }
 
 hipError_t launch_route_topk_backward(const float *logits, const uint8_t *slot_drop, const float *dtopk_w, int T,
