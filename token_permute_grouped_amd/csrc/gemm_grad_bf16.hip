@@ -33,11 +33,12 @@
 // skip the MFMAs of 32-row blocks without a live row.
 //
 // Work order.  GradGlu and GradIn take m-tiles from the tile list by tile_map, as the forward does.
-// GradWeight takes the experts largest first; 32 (or fewer) neighbouring tiles of one expert form a
-// rectangle that one XCD (block index mod 8) works on at once, sharing its row and column slabs in that L2.
+// GradWeight takes the experts largest first; runs of 32 neighbouring tiles (4 x 8) go to one XCD (block index mod
+// 8), which works on them at once and shares their row and column slabs in its L2.
 #include <type_traits>
 
 #include "gemm_common.h"
+#include "tile_list.h"
 
 namespace tpg {
 
@@ -119,24 +120,32 @@ __device__ __forceinline__ u32x4 pack8(const float *v) {
     return (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
-struct Rects {
-    int rm, rn, cols, per_expert;  // tiles of a rectangle, rectangles along n, rectangles of an expert
+// Tiles of the weight gradients: for each expert, most rows first, dW1's and then dW2's, each matrix in bands of
+// kBand tile rows, column by column.  Runs of `run` neighbouring tiles go to one XCD (block index mod 8).
+constexpr int kBand = 4;
+struct WeightTiles {
+    int n1, per_expert, total, run;  // dW1's tiles of an expert, both matrices', all, tiles of a run
 };
-__host__ __device__ inline Rects rects(int M, int N) {
-    const int nb_m = (M + kBM - 1) / kBM, nb_n = (N + kBN - 1) / kBN;
-    const int rn = nb_n < 8 ? nb_n : 8, rm = nb_m < 32 / rn ? nb_m : 32 / rn;
-    const int cols = (nb_n + rn - 1) / rn;
-    return {rm, rn, cols, cols * ((nb_m + rm - 1) / rm)};
+__host__ __device__ inline int blocks_of(int n, int size) { return (n + size - 1) / size; }
+__host__ __device__ inline WeightTiles weight_tiles(int E, bool dw1, bool dw2, int H, int I) {
+    WeightTiles t;
+    t.n1 = dw1 ? blocks_of(2 * I, kBM) * blocks_of(H, kBN) : 0;
+    t.per_expert = t.n1 + (dw2 ? blocks_of(H, kBM) * blocks_of(I, kBN) : 0);
+    t.total = E * t.per_expert;
+    t.run = t.total >= 256 ? 32 : (t.total + 7) / 8;
+    return t;
 }
 }  // namespace
 
-// order[rank] = expert, by descending row count (ties: lower expert first); one workgroup of 256
-__global__ __launch_bounds__(256) void expert_order_kernel(const int32_t *__restrict__ offsets, int E,
+// What the products need to know of the offsets, in one workgroup of 256: the m-tile list, and
+// order[rank] = expert, by descending row count (ties: lower expert first).
+__global__ __launch_bounds__(256) void grad_prepare_kernel(const int32_t *__restrict__ offsets, int E,
+                                                           int32_t *__restrict__ tiles, int32_t *__restrict__ n_tiles,
                                                            int32_t *__restrict__ order) {
-    __shared__ int cnt[256];
+    __shared__ int cnt[256], ws[8];
     const int e = threadIdx.x;
     cnt[e] = e < E ? offsets[e + 1] - offsets[e] : -1;
-    __syncthreads();
+    build_tile_list(offsets, E, kBM, 0, tiles, n_tiles, ws);  // holds a barrier
     if (e >= E) return;
     int rank = 0;
     for (int i = 0; i < E; ++i) rank += cnt[i] > cnt[e] || (cnt[i] == cnt[e] && i < e);
@@ -144,50 +153,58 @@ __global__ __launch_bounds__(256) void expert_order_kernel(const int32_t *__rest
 }
 
 struct GradArgs {
-    const uint16_t *P, *Q;   // kGlu: dy [S][H], W2 [E][H][I]; kIn: dgu [S][2I], W1 [E][2I][H];
-                             // kWeight: [S][M], [S][N] token rows
-    int M, N, K;             // kGlu, kIn: N columns of Q, K of both; kWeight: M and N columns
-    const int32_t *offsets;  // [E+1]
-    const int32_t *tiles, *n_tiles;  // kGlu, kIn: m-tiles
-    const int32_t *order;    // kWeight: experts, most rows first
-    int E;
-    uint16_t *C;             // kGlu: h [S][I]; kIn: dx [S][H]; kWeight: [E][M][N]
-    const uint16_t *gu;      // kGlu: kept pre-activations [S][2I]
-    uint16_t *dgu;           // kGlu: their gradients
-    int il;                  // kGlu: gate/up row interleave
+    const int32_t *offsets;          // [E+1]
+    const int32_t *tiles, *n_tiles;  // m-tiles of the products with token rows
+    const int32_t *order;            // experts, most rows first
+    int E, H, I;
+    const uint16_t *dy, *x, *w1, *w2, *gu;
+    uint16_t *dgu, *h;               // [S][2I], [S][I]: written by kGlu, read by the others
+    uint16_t *dx, *dw1, *dw2;        // NULL: not asked for
+    int il;                          // gate/up row interleave
     float clamp;
 };
 
+// The tile of one workgroup, `block` counted from the first workgroup of this product; lds: kStages * kStage.
 template <Grad kKind>
-__global__ __launch_bounds__(kThreads, 1) void grouped_grad_bf16_kernel(GradArgs a) {
+__device__ __forceinline__ void grad_tile(const GradArgs &a, int block, unsigned char *lds) {
     constexpr bool kW = kKind == Grad::kWeight;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];  // 160 KB
-    const int N = a.N;
 
-    // ---- tile of this workgroup: expert e, rows m0.. (of its token rows, or of its gradient), columns n0..
+    // ---- operands: P [.][ldp], Q [.][N], C [.][N]; K: sum length of kGlu and kIn
+    const uint16_t *P = kKind == Grad::kGlu ? a.dy : a.dgu, *Q = kKind == Grad::kGlu ? a.w2 : a.w1;
+    uint16_t *C = kKind == Grad::kGlu ? a.h : a.dx;
+    int ldp = kKind == Grad::kGlu ? a.H : 2 * a.I, N = kKind == Grad::kGlu ? a.I : a.H;
+
+    // ---- tile: expert e, rows m0.. (of its token rows, or of its gradient), columns n0..
     int e, m0, n0;
     if constexpr (kW) {
-        const Rects rc = rects(a.M, N);
-        const int area = rc.rm * rc.rn;
-        const int q = blockIdx.x >> 3, rect = q / area * 8 + (blockIdx.x & 7), in = q % area;
-        if (rect >= a.E * rc.per_expert) return;
-        const int re = rect % rc.per_expert;
-        e = a.order[rect / rc.per_expert];
-        m0 = ((re / rc.cols) * rc.rm + in / rc.rn) * kBM;
-        n0 = ((re % rc.cols) * rc.rn + in % rc.rn) * kBN;
-        if (m0 >= a.M || n0 >= N) return;
+        const WeightTiles wt = weight_tiles(a.E, a.dw1 != nullptr, a.dw2 != nullptr, a.H, a.I);
+        const int q = block >> 3, g = (q / wt.run * 8 + (block & 7)) * wt.run + q % wt.run;
+        if (g >= wt.total) return;
+        e = a.order[g / wt.per_expert];
+        int t = g % wt.per_expert;
+        if (t < wt.n1) {
+            P = a.dgu, Q = a.x, C = a.dw1, ldp = 2 * a.I, N = a.H;
+        } else {
+            t -= wt.n1;
+            P = a.dy, Q = a.h, C = a.dw2, ldp = a.H, N = a.I;
+        }
+        const int nb_m = blocks_of(ldp, kBM), nb_n = blocks_of(N, kBN);
+        const int band = t / (kBand * nb_n), rows = min(kBand, nb_m - band * kBand), r = t - band * kBand * nb_n;
+        m0 = (band * kBand + r % rows) * kBM;
+        n0 = r / rows * kBN;
     } else {
         int mt, nt;
-        if (!row_tile(blockIdx.x, (N + kBN - 1) / kBN, a.n_tiles, mt, nt)) return;
+        if (!row_tile(block, blocks_of(N, kBN), a.n_tiles, mt, nt)) return;
         e = a.tiles[2 * mt];
         m0 = a.tiles[2 * mt + 1];
         n0 = nt * kBN;
     }
+    const int K = ldp;
     e = __builtin_amdgcn_readfirstlane(e);
     const int64_t row0 = __builtin_amdgcn_readfirstlane(a.offsets[e]);
     const int count = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - (int)row0;
-    const int live = kW ? min(kBM, a.M - m0) : min(kBM, count - m0);  // live rows of the output tile
-    const int nk = kW ? (count + kBK - 1) / kBK : a.K / kBK;
+    const int live = kW ? min(kBM, ldp - m0) : min(kBM, count - m0);  // live rows of the output tile
+    const int nk = kW ? (count + kBK - 1) / kBK : K / kBK;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -202,10 +219,10 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_grad_bf16_kernel(GradArgs
         // GradGlu, GradIn: columns past N are not read (the last row's would lie behind the matrix)
         offQ[i] = !kW && n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
         if constexpr (kW) {
-            offP[i] = (uint32_t)(r * a.M + m0 + c) * 2u;
+            offP[i] = (uint32_t)(r * ldp + m0 + c) * 2u;
         } else {
             const int pr = wave * (kBM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
-            offP[i] = pr < live ? (uint32_t)(pr * a.K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
+            offP[i] = pr < live ? (uint32_t)(pr * K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
         }
     }
     const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
@@ -214,7 +231,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_grad_bf16_kernel(GradArgs
         if constexpr (kW) {
             const int left = __builtin_amdgcn_readfirstlane(max(0, min(kBK, count - kt * kBK)));
             const int64_t r = row0 + (left > 0 ? (int64_t)kt * kBK : 0);
-            const i32x4 p = buffer(a.P + r * a.M, left * a.M * 2), q = buffer(a.Q + r * N, left * N * 2);
+            const i32x4 p = buffer(P + r * ldp, left * ldp * 2), q = buffer(Q + r * N, left * N * 2);
 #pragma unroll
             for (int i = 0; i < kOps; ++i) {
                 dma(p, offP[i], 0, dst + i * 1024);
@@ -222,8 +239,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_grad_bf16_kernel(GradArgs
             }
         } else {
             const bool in = kt < nk;
-            const i32x4 p = buffer(a.P + (row0 + m0) * a.K, in ? live * a.K * 2 : 0);
-            const i32x4 q = buffer(a.Q + (int64_t)e * a.K * N, in ? a.K * N * 2 : 0);
+            const i32x4 p = buffer(P + (row0 + m0) * K, in ? live * K * 2 : 0);
+            const i32x4 q = buffer(Q + (int64_t)e * K * N, in ? K * N * 2 : 0);
             const int sp = in ? kt * kBK * 2 : 0, sq = in ? kt * kBK * 2 * N : 0;
 #pragma unroll
             for (int i = 0; i < kOps; ++i) {
@@ -336,7 +353,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_grad_bf16_kernel(GradArgs
                     }
                     *(u32x4 *)(a.dgu + r * 2 * N + gcol) = pack8(dg);
                     *(u32x4 *)(a.dgu + r * 2 * N + ucol) = pack8(du);
-                    *(u32x4 *)(a.C + r * N + col) = pack8(hv);
+                    *(u32x4 *)(C + r * N + col) = pack8(hv);
                 }
             }
             lds_barrier();
@@ -360,51 +377,53 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_grad_bf16_kernel(GradArgs
     lds_barrier();
     const int c = n0 + (lane & 31) * 8;
     if (c < N) {
-        uint16_t *out = a.C + ((kW ? (int64_t)e * a.M : row0) + m0) * N + c;
+        uint16_t *out = C + ((kW ? (int64_t)e * ldp : row0) + m0) * N + c;
 #pragma unroll 4
         for (int tr = wave * 2 + half; tr < kBM; tr += kWaves * 2)
             if (tr < live) *(u32x4 *)(out + (int64_t)tr * N) = *(const u32x4 *)(lds + cofs(tr, lane & 31));
     }
 }
 
-hipError_t launch_expert_order(const int32_t *offsets, int E, int32_t *order, hipStream_t s) {
-    hipLaunchKernelGGL(expert_order_kernel, dim3(1), dim3(256), 0, s, offsets, E, order);
-    return hipGetLastError();
+// GradGlu
+__global__ __launch_bounds__(kThreads, 1) void grad_glu_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];  // 160 KB
+    grad_tile<Grad::kGlu>(a, blockIdx.x, lds);
+}
+
+// GradIn (the first in_blocks workgroups) and GradWeight, which all need GradGlu's results only: in one launch
+// the small layers pay one launch's latency for three, and the large ones fill one product's last round of
+// workgroups with the next one's tiles (the weight gradients' smallest tiles come last).
+__global__ __launch_bounds__(kThreads, 1) void grad_products_kernel(GradArgs a, int in_blocks) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];
+    if ((int)blockIdx.x < in_blocks)
+        grad_tile<Grad::kIn>(a, blockIdx.x, lds);
+    else
+        grad_tile<Grad::kWeight>(a, blockIdx.x - in_blocks, lds);
 }
 
 namespace {
-template <Grad kKind>
-hipError_t launch_rows(const GradArgs &a, int64_t max_tiles, hipStream_t s) {
-    const TileMap tm = tile_map((a.N + kBN - 1) / kBN);
-    const int64_t blocks = (max_tiles + tm.gm - 1) / tm.gm * tm.per_band;
-    hipLaunchKernelGGL(grouped_grad_bf16_kernel<kKind>, dim3(blocks), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+int64_t row_blocks(int64_t max_tiles, int N) {
+    const TileMap tm = tile_map(blocks_of(N, kBN));
+    return (max_tiles + tm.gm - 1) / tm.gm * tm.per_band;
 }
 }  // namespace
 
-hipError_t launch_grad_glu_bf16(const uint16_t *dy, const uint16_t *w2, const uint16_t *gu, const int32_t *offsets,
-                                const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
-                                int glu_interleave, float clamp, uint16_t *dgu, uint16_t *h, hipStream_t s) {
-    GradArgs a = {};
-    a.P = dy, a.Q = w2, a.N = I, a.K = H, a.offsets = offsets, a.tiles = tiles, a.n_tiles = n_tiles;
-    a.C = h, a.gu = gu, a.dgu = dgu, a.il = glu_interleave, a.clamp = clamp;
-    return launch_rows<Grad::kGlu>(a, max_tiles, s);
-}
-
-hipError_t launch_grad_in_bf16(const uint16_t *dgu, const uint16_t *w1, const int32_t *offsets, const int32_t *tiles,
-                               const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *dx, hipStream_t s) {
-    GradArgs a = {};
-    a.P = dgu, a.Q = w1, a.N = H, a.K = 2 * I, a.offsets = offsets, a.tiles = tiles, a.n_tiles = n_tiles, a.C = dx;
-    return launch_rows<Grad::kIn>(a, max_tiles, s);
-}
-
-hipError_t launch_grad_weight_bf16(const uint16_t *p, int M, const uint16_t *q, int N, const int32_t *offsets,
-                                   const int32_t *order, int E, uint16_t *dw, hipStream_t s) {
-    const Rects rc = rects(M, N);
-    const int64_t blocks = ((int64_t)E * rc.per_expert + 7) / 8 * 8 * rc.rm * rc.rn;
-    GradArgs a = {};
-    a.P = p, a.Q = q, a.M = M, a.N = N, a.offsets = offsets, a.order = order, a.E = E, a.C = dw;
-    hipLaunchKernelGGL(grouped_grad_bf16_kernel<Grad::kWeight>, dim3(blocks), dim3(kThreads), 0, s, a);
+hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const uint16_t *gu, const int32_t *offsets,
+                                    const moe_weights &w, const moe_problem &p, int32_t *tiles, int32_t *n_tiles,
+                                    int32_t *order, uint16_t *dgu, uint16_t *h, uint16_t *dx, uint16_t *dw1,
+                                    uint16_t *dw2, hipStream_t s) {
+    const GradArgs a = {offsets, tiles, n_tiles, order, p.E, p.H, p.I, dy, x, (const uint16_t *)w.w1,
+                        (const uint16_t *)w.w2, gu, dgu, h, dx, dw1, dw2, p.glu_interleave, p.swiglu_clamp};
+    const int64_t max_tiles = max_m_tiles(p);
+    hipLaunchKernelGGL(grad_prepare_kernel, dim3(1), dim3(256), 0, s, offsets, p.E, tiles, n_tiles, order);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(grad_glu_kernel, dim3(row_blocks(max_tiles, p.I)), dim3(kThreads), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t in_blocks = dx ? row_blocks(max_tiles, p.H) : 0;
+    const WeightTiles wt = weight_tiles(p.E, dw1 != nullptr, dw2 != nullptr, p.H, p.I);
+    const int64_t w_blocks = wt.total ? ((int64_t)wt.total + 8 * wt.run - 1) / (8 * wt.run) * (8 * wt.run) : 0;
+    hipLaunchKernelGGL(grad_products_kernel, dim3(in_blocks + w_blocks), dim3(kThreads), 0, s, a, (int)in_blocks);
     return hipGetLastError();
 }
 

@@ -586,26 +586,10 @@ int moe_grouped_ffn_backward(const void *dy_perm, const void *x_perm, const void
     if (ws_bytes < moe_call_workspace_bytes(p, MOE_WS_FFN_BACKWARD)) return MOE_ERR_WORKSPACE;
     const BackwardLayout L = backward_layout(*p);
     char *b = (char *)ws;
-    int32_t *tiles = (int32_t *)(b + L.tiles), *n_tiles = (int32_t *)(b + L.n_tiles);
-    int32_t *order = (int32_t *)(b + L.order);
-    uint16_t *dgu = (uint16_t *)(b + L.dgu), *h = (uint16_t *)(b + L.h);
-    const int64_t max_tiles = max_m_tiles(*p);
-    st = hip_status(launch_build_tiles(offsets, p->E, gemm_bm(*p), tile_order(*p), tiles, n_tiles, stream));
-    if (!st && (dw1 || dw2)) st = hip_status(launch_expert_order(offsets, p->E, order, stream));
-    if (!st)
-        st = hip_status(launch_grad_glu_bf16((const uint16_t *)dy_perm, (const uint16_t *)w->w2, (const uint16_t *)gu,
-                                             offsets, tiles, n_tiles, max_tiles, p->H, p->I, p->glu_interleave,
-                                             p->swiglu_clamp, dgu, h, stream));
-    if (!st && dx_perm)
-        st = hip_status(launch_grad_in_bf16(dgu, (const uint16_t *)w->w1, offsets, tiles, n_tiles, max_tiles, p->H,
-                                            p->I, (uint16_t *)dx_perm, stream));
-    if (!st && dw1)
-        st = hip_status(launch_grad_weight_bf16(dgu, 2 * p->I, (const uint16_t *)x_perm, p->H, offsets, order, p->E,
-                                                (uint16_t *)dw1, stream));
-    if (!st && dw2)
-        st = hip_status(launch_grad_weight_bf16((const uint16_t *)dy_perm, p->H, h, p->I, offsets, order, p->E,
-                                                (uint16_t *)dw2, stream));
-    return st;
+    return hip_status(launch_grouped_grad_bf16(
+        (const uint16_t *)dy_perm, (const uint16_t *)x_perm, (const uint16_t *)gu, offsets, *w, *p,
+        (int32_t *)(b + L.tiles), (int32_t *)(b + L.n_tiles), (int32_t *)(b + L.order), (uint16_t *)(b + L.dgu),
+        (uint16_t *)(b + L.h), (uint16_t *)dx_perm, (uint16_t *)dw1, (uint16_t *)dw2, stream));
 }
 
 int moe_w4a8_dequant_table(uint8_t *out8, hipStream_t stream) {

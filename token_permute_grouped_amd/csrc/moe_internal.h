@@ -130,18 +130,12 @@ hipError_t launch_gemm2_bf16(const uint16_t *h, const uint16_t *w2, const int32_
                              const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *y_perm,
                              const int32_t *row_dst, hipStream_t s);
 
-// Backward pass.  grad_glu: dh = dy W2, then dgu [S][2I] (stored row order) from dh and the kept gu, and
-// h [S][I] again; grad_in: dx = dgu W1
-hipError_t launch_grad_glu_bf16(const uint16_t *dy, const uint16_t *w2, const uint16_t *gu, const int32_t *offsets,
-                                const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
-                                int glu_interleave, float clamp, uint16_t *dgu, uint16_t *h, hipStream_t s);
-hipError_t launch_grad_in_bf16(const uint16_t *dgu, const uint16_t *w1, const int32_t *offsets, const int32_t *tiles,
-                               const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *dx, hipStream_t s);
-// Weight gradient of every expert: dw[e][m][n] = sum over e's rows r of p[r][m] q[r][n]; p [S][M],
-// q [S][N], dw [E][M][N]; M and N multiples of 128.  order [E]: the experts, most rows first.
-hipError_t launch_expert_order(const int32_t *offsets, int E, int32_t *order, hipStream_t s);
-hipError_t launch_grad_weight_bf16(const uint16_t *p, int M, const uint16_t *q, int N, const int32_t *offsets,
-                                   const int32_t *order, int E, uint16_t *dw, hipStream_t s);
+// The grouped FFN's backward pass: tiles, n_tiles, order [E], dgu [S][2I] and h [S][I] are scratch; dx, dw1 and dw2
+// may be NULL
+hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const uint16_t *gu, const int32_t *offsets,
+                                    const moe_weights &w, const moe_problem &p, int32_t *tiles, int32_t *n_tiles,
+                                    int32_t *order, uint16_t *dgu, uint16_t *h, uint16_t *dx, uint16_t *dw1,
+                                    uint16_t *dw2, hipStream_t s);
 
 // row_src NULL: x_perm / x_perm_scale are the expert-ordered rows; else x / x_scale token rows
 // read through row_src (the gather fused into GEMM1; needs gather_fits_fp8(T, H)).  row_dst as
