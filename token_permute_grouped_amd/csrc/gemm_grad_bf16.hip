@@ -51,7 +51,7 @@ constexpr int kStages = 5;
 constexpr int kOps = kHalf / 1024 / kWaves;  // DMAs per wave, stage and operand (2)
 static_assert(kBM * kBK * 2 == kHalf && kBN * 2 == 512, "both operand layouts fill the same 16 KB");
 
-enum class Grad { kGlu, kIn, kWeight };
+enum class Grad { kGlu, kIn };
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -121,10 +121,12 @@ __device__ __forceinline__ u32x4 pack8(const float *v) {
 }
 
 // Tiles of the weight gradients: for each expert, most rows first, dW1's and then dW2's, each matrix in bands of
-// kBand tile rows, column by column.  Runs of `run` neighbouring tiles go to one XCD (block index mod 8).
+// kBand tile rows, column by column.  Runs of `run` neighbouring tiles go to one XCD (block index mod 8), a tile to a
+// workgroup; the `blocks` workgroups walk over the list, XCDs 0 to 7 and back, so that none of them always gets the
+// larger of two experts.
 constexpr int kBand = 4;
 struct WeightTiles {
-    int n1, per_expert, total, run;  // dW1's tiles of an expert, both matrices', all, tiles of a run
+    int n1, per_expert, total, run, blocks;  // n1: dW1's tiles of an expert; per_expert: both matrices'
 };
 __host__ __device__ inline int blocks_of(int n, int size) { return (n + size - 1) / size; }
 __host__ __device__ inline WeightTiles weight_tiles(int E, bool dw1, bool dw2, int H, int I) {
@@ -133,15 +135,21 @@ __host__ __device__ inline WeightTiles weight_tiles(int E, bool dw1, bool dw2, i
     t.per_expert = t.n1 + (dw2 ? blocks_of(H, kBM) * blocks_of(I, kBN) : 0);
     t.total = E * t.per_expert;
     t.run = t.total >= 256 ? 32 : (t.total + 7) / 8;
+    t.blocks = 8 * t.run;
     return t;
+}
+// tile that workgroup `block` works on in step i
+__device__ __forceinline__ int weight_tile_index(const WeightTiles &t, int block, int i) {
+    const int xcd = block & 7;
+    return (i * 8 + (i & 1 ? 7 - xcd : xcd)) * t.run + (block >> 3);
 }
 }  // namespace
 
 // What the products need to know of the offsets, in one workgroup of 256: the m-tile list, and
-// order[rank] = expert, by descending row count (ties: lower expert first).
+// order[rank] = {expert, first row, rows}, by descending row count (ties: lower expert first).
 __global__ __launch_bounds__(256) void grad_prepare_kernel(const int32_t *__restrict__ offsets, int E,
                                                            int32_t *__restrict__ tiles, int32_t *__restrict__ n_tiles,
-                                                           int32_t *__restrict__ order) {
+                                                           int4 *__restrict__ order) {
     __shared__ int cnt[256], ws[8];
     const int e = threadIdx.x;
     cnt[e] = e < E ? offsets[e + 1] - offsets[e] : -1;
@@ -149,13 +157,13 @@ __global__ __launch_bounds__(256) void grad_prepare_kernel(const int32_t *__rest
     if (e >= E) return;
     int rank = 0;
     for (int i = 0; i < E; ++i) rank += cnt[i] > cnt[e] || (cnt[i] == cnt[e] && i < e);
-    order[rank] = e;
+    order[rank] = make_int4(e, offsets[e], cnt[e], 0);
 }
 
 struct GradArgs {
     const int32_t *offsets;          // [E+1]
     const int32_t *tiles, *n_tiles;  // m-tiles of the products with token rows
-    const int32_t *order;            // experts, most rows first
+    const int4 *order;               // {expert, first row, rows}, most rows first
     int E, H, I;
     const uint16_t *dy, *x, *w1, *w2, *gu;
     uint16_t *dgu, *h;               // [S][2I], [S][I]: written by kGlu, read by the others
@@ -164,47 +172,21 @@ struct GradArgs {
     float clamp;
 };
 
-// The tile of one workgroup, `block` counted from the first workgroup of this product; lds: kStages * kStage.
+// One tile of GradGlu or GradIn; lds: kStages * kStage.
 template <Grad kKind>
-__device__ __forceinline__ void grad_tile(const GradArgs &a, int block, unsigned char *lds) {
-    constexpr bool kW = kKind == Grad::kWeight;
-
-    // ---- operands: P [.][ldp], Q [.][N], C [.][N]; K: sum length of kGlu and kIn
+__device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsigned char *lds) {
+    // ---- operands P [S][K], Q [E][K][N], C [S][N]; tile: rows m0.. of expert e, columns n0..
     const uint16_t *P = kKind == Grad::kGlu ? a.dy : a.dgu, *Q = kKind == Grad::kGlu ? a.w2 : a.w1;
     uint16_t *C = kKind == Grad::kGlu ? a.h : a.dx;
-    int ldp = kKind == Grad::kGlu ? a.H : 2 * a.I, N = kKind == Grad::kGlu ? a.I : a.H;
-
-    // ---- tile: expert e, rows m0.. (of its token rows, or of its gradient), columns n0..
-    int e, m0, n0;
-    if constexpr (kW) {
-        const WeightTiles wt = weight_tiles(a.E, a.dw1 != nullptr, a.dw2 != nullptr, a.H, a.I);
-        const int q = block >> 3, g = (q / wt.run * 8 + (block & 7)) * wt.run + q % wt.run;
-        if (g >= wt.total) return;
-        e = a.order[g / wt.per_expert];
-        int t = g % wt.per_expert;
-        if (t < wt.n1) {
-            P = a.dgu, Q = a.x, C = a.dw1, ldp = 2 * a.I, N = a.H;
-        } else {
-            t -= wt.n1;
-            P = a.dy, Q = a.h, C = a.dw2, ldp = a.H, N = a.I;
-        }
-        const int nb_m = blocks_of(ldp, kBM), nb_n = blocks_of(N, kBN);
-        const int band = t / (kBand * nb_n), rows = min(kBand, nb_m - band * kBand), r = t - band * kBand * nb_n;
-        m0 = (band * kBand + r % rows) * kBM;
-        n0 = r / rows * kBN;
-    } else {
-        int mt, nt;
-        if (!row_tile(block, blocks_of(N, kBN), a.n_tiles, mt, nt)) return;
-        e = a.tiles[2 * mt];
-        m0 = a.tiles[2 * mt + 1];
-        n0 = nt * kBN;
-    }
-    const int K = ldp;
-    e = __builtin_amdgcn_readfirstlane(e);
+    const int K = kKind == Grad::kGlu ? a.H : 2 * a.I, N = kKind == Grad::kGlu ? a.I : a.H;
+    int mt, nt;
+    if (!row_tile(block, blocks_of(N, kBN), a.n_tiles, mt, nt)) return;
+    const int e = __builtin_amdgcn_readfirstlane(a.tiles[2 * mt]);
+    const int m0 = __builtin_amdgcn_readfirstlane(a.tiles[2 * mt + 1]), n0 = nt * kBN;
     const int64_t row0 = __builtin_amdgcn_readfirstlane(a.offsets[e]);
     const int count = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - (int)row0;
-    const int live = kW ? min(kBM, ldp - m0) : min(kBM, count - m0);  // live rows of the output tile
-    const int nk = kW ? (count + kBK - 1) / kBK : K / kBK;
+    const int live = min(kBM, count - m0);  // live rows of the tile
+    const int nk = K / kBK;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -216,37 +198,22 @@ __device__ __forceinline__ void grad_tile(const GradArgs &a, int block, unsigned
 #pragma unroll
     for (int i = 0; i < kOps; ++i) {
         const int r = wave * (kBK / kWaves) + i * 2 + half, c = tchunk(r, lane & 31) * 8;  // stage row, column
-        // GradGlu, GradIn: columns past N are not read (the last row's would lie behind the matrix)
-        offQ[i] = !kW && n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
-        if constexpr (kW) {
-            offP[i] = (uint32_t)(r * ldp + m0 + c) * 2u;
-        } else {
-            const int pr = wave * (kBM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
-            offP[i] = pr < live ? (uint32_t)(pr * K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
-        }
+        // columns past N are not read (the last row's would lie behind the matrix)
+        offQ[i] = n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
+        const int pr = wave * (kBM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
+        offP[i] = pr < live ? (uint32_t)(pr * K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
     }
     const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
     auto request = [&](int kt, int slot) {
         const uint32_t dst = lds0 + slot * kStage;
-        if constexpr (kW) {
-            const int left = __builtin_amdgcn_readfirstlane(max(0, min(kBK, count - kt * kBK)));
-            const int64_t r = row0 + (left > 0 ? (int64_t)kt * kBK : 0);
-            const i32x4 p = buffer(P + r * ldp, left * ldp * 2), q = buffer(Q + r * N, left * N * 2);
+        const bool in = kt < nk;
+        const i32x4 p = buffer(P + (row0 + m0) * K, in ? live * K * 2 : 0);
+        const i32x4 q = buffer(Q + (int64_t)e * K * N, in ? K * N * 2 : 0);
+        const int sp = in ? kt * kBK * 2 : 0, sq = in ? kt * kBK * 2 * N : 0;
 #pragma unroll
-            for (int i = 0; i < kOps; ++i) {
-                dma(p, offP[i], 0, dst + i * 1024);
-                dma(q, offQ[i], 0, dst + kHalf + i * 1024);
-            }
-        } else {
-            const bool in = kt < nk;
-            const i32x4 p = buffer(P + (row0 + m0) * K, in ? live * K * 2 : 0);
-            const i32x4 q = buffer(Q + (int64_t)e * K * N, in ? K * N * 2 : 0);
-            const int sp = in ? kt * kBK * 2 : 0, sq = in ? kt * kBK * 2 * N : 0;
-#pragma unroll
-            for (int i = 0; i < kOps; ++i) {
-                dma(p, offP[i], sp, dst + i * 1024);
-                dma(q, offQ[i], sq, dst + kHalf + i * 1024);
-            }
+        for (int i = 0; i < kOps; ++i) {
+            dma(p, offP[i], sp, dst + i * 1024);
+            dma(q, offQ[i], sq, dst + kHalf + i * 1024);
         }
     };
 
@@ -261,7 +228,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs &a, int block, unsigned
     // NB: 32-row blocks of this wave with a live row
     auto mainloop = [&](auto nb_tag) {
         constexpr int NB = decltype(nb_tag)::value;
-        constexpr int NR = (kW ? 2 : 1) * NB + 4, NM = 2 * NB;  // LDS reads and MFMAs of a step
+        constexpr int NR = NB + 4, NM = 2 * NB;  // LDS reads and MFMAs of a step
         constexpr int G = 2 * kOps;                            // DMAs of a stage
         bf16x8 fq[2][2], fp[2][NB > 0 ? NB : 1];
         auto load = [&](int buf, int slot, int ks) {
@@ -271,7 +238,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs &a, int block, unsigned
                 for (int x = 0; x < 2; ++x) fq[buf][x] = load_trans(s + kHalf, wn * 64 + x * 32, ks, lane);
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    fp[buf][b] = kW ? load_trans(s, wm * 128 + b * 32, ks, lane) : load_rows(s, wm * 128 + b * 32, ks, lane);
+                    fp[buf][b] = load_rows(s, wm * 128 + b * 32, ks, lane);
             }
         };
         auto mfmas = [&](int buf) {
@@ -301,12 +268,12 @@ __device__ __forceinline__ void grad_tile(const GradArgs &a, int block, unsigned
         }
         wait_vmcnt<0>();  // the LDS is written again below
     };
-    switch (kW ? 4 : max(0, min(4, (live - wm * 128 + 31) >> 5))) {
+    switch (max(0, min(4, (live - wm * 128 + 31) >> 5))) {
         case 4: mainloop(std::integral_constant<int, 4>{}); break;
-        case 3: if constexpr (!kW) mainloop(std::integral_constant<int, 3>{}); break;
-        case 2: if constexpr (!kW) mainloop(std::integral_constant<int, 2>{}); break;
-        case 1: if constexpr (!kW) mainloop(std::integral_constant<int, 1>{}); break;
-        default: if constexpr (!kW) mainloop(std::integral_constant<int, 0>{}); break;
+        case 3: mainloop(std::integral_constant<int, 3>{}); break;
+        case 2: mainloop(std::integral_constant<int, 2>{}); break;
+        case 1: mainloop(std::integral_constant<int, 1>{}); break;
+        default: mainloop(std::integral_constant<int, 0>{}); break;
     }
 
     // ---- epilogue: lane holds tile row wm 128 + b 32 + (lane & 31) and columns wn 64 + x 32 + 8 (v >> 2) +
@@ -377,17 +344,193 @@ __device__ __forceinline__ void grad_tile(const GradArgs &a, int block, unsigned
     lds_barrier();
     const int c = n0 + (lane & 31) * 8;
     if (c < N) {
-        uint16_t *out = C + ((kW ? (int64_t)e * ldp : row0) + m0) * N + c;
+        uint16_t *out = C + (row0 + m0) * N + c;
 #pragma unroll 4
         for (int tr = wave * 2 + half; tr < kBM; tr += kWaves * 2)
             if (tr < live) *(u32x4 *)(out + (int64_t)tr * N) = *(const u32x4 *)(lds + cofs(tr, lane & 31));
     }
 }
 
+// A tile of dW1 or dW2: C[m0..][n0..] = sum over `count` rows of P[r][m] Q[r][n], both from their first row
+struct WeightTile {
+    const uint16_t *P, *Q;  // first row of the expert, first column of the tile
+    uint16_t *C;            // first row and column of the tile
+    int ldp, N, rows, cols; // row lengths; live rows and columns of the tile
+    int count;              // rows summed over; 0 for a tile behind the last
+    int nk;                 // stages
+    bool live;
+};
+__device__ __forceinline__ WeightTile weight_tile(const GradArgs &a, const WeightTiles &wt, int g) {
+    WeightTile w = {};
+    w.live = g < wt.total;
+    if (!w.live) return w;
+    // through the constant address space: a scalar load, which the DMAs' counter does not see
+    const i32x4 o = ((const __attribute__((address_space(4))) i32x4 *)(uintptr_t)a.order)[g / wt.per_expert];
+    int t = g % wt.per_expert;
+    const bool first = t < wt.n1;
+    if (!first) t -= wt.n1;
+    w.ldp = first ? 2 * a.I : a.H;
+    w.N = first ? a.H : a.I;
+    const int nb_m = blocks_of(w.ldp, kBM), nb_n = blocks_of(w.N, kBN);
+    const int band = t / (kBand * nb_n), rows = min(kBand, nb_m - band * kBand), r = t - band * kBand * nb_n;
+    const int m0 = (band * kBand + r % rows) * kBM, n0 = r / rows * kBN;
+    const int e = __builtin_amdgcn_readfirstlane(o.x);
+    const int64_t row0 = __builtin_amdgcn_readfirstlane(o.y);
+    w.count = __builtin_amdgcn_readfirstlane(o.z);
+    w.nk = blocks_of(w.count, kBK);
+    w.P = (first ? a.dgu : a.dy) + row0 * w.ldp + m0;
+    w.Q = (first ? a.x : a.h) + row0 * w.N + n0;
+    w.C = (first ? a.dw1 : a.dw2) + ((int64_t)e * w.ldp + m0) * w.N + n0;
+    w.rows = min(kBM, w.ldp - m0);
+    w.cols = min(kBN, w.N - n0);
+    return w;
+}
+
+// The weight gradients' tiles of one workgroup, one after the other; lds: kStages * kStage.
+//
+// The ring runs on from one tile to the next: while a tile's last stages are multiplied, the first four of the next
+// are requested, so its data is there when the tile has been stored.  A tile takes L = max(nk, 4) places of the
+// ring, of which the places nk.. are left to requests out of bounds; place n of it, for n = L .. L + 3, is the next
+// tile's n - L, and place L + 4 stays free until the tile has gone through it to memory, 64 rows at a time.
+// Waiting for fewer than n outstanding requests is right whatever the stores do: they only make the count larger.
+// (One tile per workgroup, with the whole ring filled and drained for each: 8 us more per tile.)
+__device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, unsigned char *lds) {
+    const WeightTiles wt = weight_tiles(a.E, a.dw1 != nullptr, a.dw2 != nullptr, a.H, a.I);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / kWaveN, wn = wave % kWaveN;
+    const int half = lane >> 5;
+    constexpr int G = 2 * kOps;  // DMAs of a stage
+
+    int sr[kOps], sc[kOps];  // stage row and column byte of this lane's DMAs
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) {
+        sr[i] = wave * (kBK / kWaves) + i * 2 + half;
+        sc[i] = tchunk(sr[i], lane & 31) * 16;
+    }
+    const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
+    auto request = [&](const WeightTile &w, int kt, int slot) {
+        const uint32_t dst = lds0 + slot * kStage;
+        const int left = __builtin_amdgcn_readfirstlane(max(0, min(kBK, w.count - kt * kBK)));
+        const int64_t r = left > 0 ? (int64_t)kt * kBK : 0;
+        // bounds from the tile's first column: the last row's bytes end with the tile's columns
+        const i32x4 p = buffer(w.P + r * w.ldp, left > 0 ? (left - 1) * w.ldp * 2 + w.rows * 2 : 0);
+        const i32x4 q = buffer(w.Q + r * w.N, left > 0 ? (left - 1) * w.N * 2 + w.cols * 2 : 0);
+#pragma unroll
+        for (int i = 0; i < kOps; ++i) {
+            dma(p, (uint32_t)(sr[i] * w.ldp * 2 + sc[i]), 0, dst + i * 1024);
+            dma(q, (uint32_t)(sr[i] * w.N * 2 + sc[i]), 0, dst + kHalf + i * 1024);
+        }
+    };
+
+    bf16x8 fq[2][2], fp[2][4];
+    f32x16 acc[2][4];
+    auto load = [&](int buf, int slot, int ks) {
+        const unsigned char *s = lds + slot * kStage;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) fq[buf][x] = load_trans(s + kHalf, wn * 64 + x * 32, ks, lane);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) fp[buf][b] = load_trans(s, wm * 128 + b * 32, ks, lane);
+    };
+    auto mfmas = [&](int buf) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                acc[x][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[buf][x], fp[buf][b], acc[x][b], 0, 0, 0);
+    };
+    auto ring = [](int slot) { return slot >= kStages ? slot - kStages : slot; };
+
+    int step = 0;
+    WeightTile cur = weight_tile(a, wt, weight_tile_index(wt, block, 0));
+    WeightTile next = weight_tile(a, wt, weight_tile_index(wt, block, 1));
+    if (!cur.live) return;
+    int base = 0;  // ring slot of the tile's place 0
+    auto place = [&](int n, int L, int slot) {  // requests place n of the current tile
+        if (n < L) request(cur, n, slot);
+        else request(next, n - L, slot);
+    };
+    for (int n = 0; n < 4; ++n) place(n, max(cur.nk, 4), n);
+    while (true) {
+        const int nk = cur.nk, L = max(nk, 4);
+        place(4, L, ring(base + 4));
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[x][b][v] = 0.f;
+        wait_vmcnt<(kStages - 1) * G>();  // place 0 has landed
+        lds_barrier();
+        int slot = base;
+        if (nk > 0) {
+            load(0, slot, 0);
+            for (int kt = 0; kt + 1 < nk; ++kt) {
+                load(1, slot, 1);
+                mfmas(0);
+                interleave_ds_mfma<12, 8>();
+                wait_vmcnt<(kStages - 2) * G>();  // place kt+1 has landed; kt+2 .. kt+4 may be in flight
+                lds_barrier();
+                place(kt + kStages, L, slot);
+                slot = ring(slot + 1);
+                load(0, slot, 0);
+                mfmas(1);
+                interleave_ds_mfma<12, 8>();
+            }
+            load(1, slot, 1);
+            mfmas(0);
+            interleave_ds_mfma<12, 8>();
+            mfmas(1);
+            slot = ring(slot + 1);
+        }
+        // a short tile's remaining places; the last one's is left free
+        if (nk > 0 && nk < L) lds_barrier();  // every wave has read place nk - 1
+        for (int kt = nk > 0 ? nk - 1 : 0; kt + 1 < L; ++kt) place(kt + kStages, L, ring(base + kt % kStages));
+        base = ring(base + L % kStages);
+        const int stage_slot = ring(base + 4);  // place L + 4
+        const WeightTile done = cur;
+        cur = next;
+        next = weight_tile(a, wt, weight_tile_index(wt, block, ++step + 1));
+
+        // ---- store: a lane holds row wm 128 + b 32 + (lane & 31) and columns wn 64 + x 32 + 8 (v >> 2) + 4 (lane >>
+        //      5) + (v & 3); block row b of both wave rows goes through the free place at a time
+        wait_vmcnt<(kStages - 1) * G>();  // nothing is on its way to it
+        unsigned char *st = lds + stage_slot * kStage;
+        auto cofs = [](int r, int c) { return r * (kBN * 2) + ((c ^ (r & 15)) << 4); };
+        const int lr = wm * 32 + (lane & 31);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            lds_barrier();  // every wave is done with the slot
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int g4 = 0; g4 < 4; ++g4) {
+                    u32x2 o;
+                    o.x = pack_bf16x2(acc[x][b][g4 * 4 + 0], acc[x][b][g4 * 4 + 1]);
+                    o.y = pack_bf16x2(acc[x][b][g4 * 4 + 2], acc[x][b][g4 * 4 + 3]);
+                    *(u32x2 *)(st + cofs(lr, wn * 8 + x * 4 + g4) + half * 8) = o;
+                }
+            lds_barrier();
+            if ((lane & 31) * 8 < done.cols) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = wave * 2 + half + i * 16, row = (r >> 5) * 128 + b * 32 + (r & 31);
+                    if (row < done.rows)
+                        *(u32x4 *)(done.C + (int64_t)row * done.N + (lane & 31) * 8) =
+                            *(const u32x4 *)(st + cofs(r, lane & 31));
+                }
+            }
+        }
+        if (!cur.live) break;
+        lds_barrier();  // the slot takes place 4 of the next tile
+    }
+    wait_vmcnt<0>();  // requests still write to this workgroup's LDS
+}
+
 // GradGlu
 __global__ __launch_bounds__(kThreads, 1) void grad_glu_kernel(GradArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];  // 160 KB
-    grad_tile<Grad::kGlu>(a, blockIdx.x, lds);
+    grad_row_tile<Grad::kGlu>(a, blockIdx.x, lds);
 }
 
 // GradIn (the first in_blocks workgroups) and GradWeight, which all need GradGlu's results only: in one launch
@@ -396,9 +539,9 @@ __global__ __launch_bounds__(kThreads, 1) void grad_glu_kernel(GradArgs a) {
 __global__ __launch_bounds__(kThreads, 1) void grad_products_kernel(GradArgs a, int in_blocks) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];
     if ((int)blockIdx.x < in_blocks)
-        grad_tile<Grad::kIn>(a, blockIdx.x, lds);
+        grad_row_tile<Grad::kIn>(a, blockIdx.x, lds);
     else
-        grad_tile<Grad::kWeight>(a, blockIdx.x - in_blocks, lds);
+        grad_weight_tiles(a, blockIdx.x - in_blocks, lds);
 }
 
 namespace {
@@ -412,18 +555,17 @@ hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const
                                     const moe_weights &w, const moe_problem &p, int32_t *tiles, int32_t *n_tiles,
                                     int32_t *order, uint16_t *dgu, uint16_t *h, uint16_t *dx, uint16_t *dw1,
                                     uint16_t *dw2, hipStream_t s) {
-    const GradArgs a = {offsets, tiles, n_tiles, order, p.E, p.H, p.I, dy, x, (const uint16_t *)w.w1,
+    const GradArgs a = {offsets, tiles, n_tiles, (const int4 *)order, p.E, p.H, p.I, dy, x, (const uint16_t *)w.w1,
                         (const uint16_t *)w.w2, gu, dgu, h, dx, dw1, dw2, p.glu_interleave, p.swiglu_clamp};
     const int64_t max_tiles = max_m_tiles(p);
-    hipLaunchKernelGGL(grad_prepare_kernel, dim3(1), dim3(256), 0, s, offsets, p.E, tiles, n_tiles, order);
+    hipLaunchKernelGGL(grad_prepare_kernel, dim3(1), dim3(256), 0, s, offsets, p.E, tiles, n_tiles, (int4 *)order);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(grad_glu_kernel, dim3(row_blocks(max_tiles, p.I)), dim3(kThreads), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t in_blocks = dx ? row_blocks(max_tiles, p.H) : 0;
     const WeightTiles wt = weight_tiles(p.E, dw1 != nullptr, dw2 != nullptr, p.H, p.I);
-    const int64_t w_blocks = wt.total ? ((int64_t)wt.total + 8 * wt.run - 1) / (8 * wt.run) * (8 * wt.run) : 0;
-    hipLaunchKernelGGL(grad_products_kernel, dim3(in_blocks + w_blocks), dim3(kThreads), 0, s, a, (int)in_blocks);
+    hipLaunchKernelGGL(grad_products_kernel, dim3(in_blocks + wt.blocks), dim3(kThreads), 0, s, a, (int)in_blocks);
     return hipGetLastError();
 }
 

@@ -102,7 +102,7 @@ BackwardLayout backward_layout(const moe_problem &p) {
     L.n_tiles = o;
     o = align256(o + 16);
     L.order = o;
-    o = align256(o + (size_t)p.E * 4);
+    o = align256(o + (size_t)p.E * 16);
     L.dgu = o;
     o = align256(o + S * 2 * (size_t)p.I * 2);
     L.h = o;

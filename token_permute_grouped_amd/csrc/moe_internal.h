@@ -130,7 +130,7 @@ hipError_t launch_gemm2_bf16(const uint16_t *h, const uint16_t *w2, const int32_
                              const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *y_perm,
                              const int32_t *row_dst, hipStream_t s);
 
-// The grouped FFN's backward pass: tiles, n_tiles, order [E], dgu [S][2I] and h [S][I] are scratch; dx, dw1 and dw2
+// The grouped FFN's backward pass: tiles, n_tiles, order [E][4], dgu [S][2I] and h [S][I] are scratch; dx, dw1 and dw2
 // may be NULL
 hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const uint16_t *gu, const int32_t *offsets,
                                     const moe_weights &w, const moe_problem &p, int32_t *tiles, int32_t *n_tiles,
