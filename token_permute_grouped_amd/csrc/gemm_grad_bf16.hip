@@ -204,16 +204,19 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
         offP[i] = pr < live ? (uint32_t)(pr * K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
     }
     const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
-    auto request = [&](int kt, int slot) {
+    i32x4 rp = buffer(P + (row0 + m0) * K, live * K * 2), rq = buffer(Q + (int64_t)e * K * N, K * N * 2);
+    int sp = 0, sq = 0, left = nk;  // the next stage's offsets in P's rows and in Q, and stages left
+    auto request = [&](int slot) {
         const uint32_t dst = lds0 + slot * kStage;
-        const bool in = kt < nk;
-        const i32x4 p = buffer(P + (row0 + m0) * K, in ? live * K * 2 : 0);
-        const i32x4 q = buffer(Q + (int64_t)e * K * N, in ? K * N * 2 : 0);
-        const int sp = in ? kt * kBK * 2 : 0, sq = in ? kt * kBK * 2 * N : 0;
+        if (left == 0) rp.z = rq.z = 0;  // behind the last stage: out of bounds, nothing is read
 #pragma unroll
         for (int i = 0; i < kOps; ++i) {
-            dma(p, offP[i], sp, dst + i * 1024);
-            dma(q, offQ[i], sq, dst + kHalf + i * 1024);
+            dma(rp, offP[i], sp, dst + i * 1024);
+            dma(rq, offQ[i], sq, dst + kHalf + i * 1024);
+        }
+        if (--left > 0) {
+            sp += kBK * 2;
+            sq += kBK * 2 * N;
         }
     };
 
@@ -249,7 +252,7 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
                     acc[x][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[buf][x], fp[buf][b], acc[x][b], 0, 0, 0);
         };
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) request(s, s);
+        for (int s = 0; s < kStages; ++s) request(s);
         wait_vmcnt<(kStages - 1) * G>();
         lds_barrier();
         load(0, 0, 0);
@@ -260,7 +263,7 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
             if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
             wait_vmcnt<(kStages - 2) * G>();  // stage kt+1 has landed; kt+2 .. kt+4 may be in flight
             lds_barrier();
-            request(kt + kStages, slot);
+            request(slot);
             slot = slot + 1 == kStages ? 0 : slot + 1;
             load(0, slot, 0);
             mfmas(1);
@@ -409,18 +412,32 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
         sc[i] = tchunk(sr[i], lane & 31) * 16;
     }
     const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
-    auto request = [&](const WeightTile &w, int kt, int slot) {
-        const uint32_t dst = lds0 + slot * kStage;
-        const int left = __builtin_amdgcn_readfirstlane(max(0, min(kBK, w.count - kt * kBK)));
-        const int64_t r = left > 0 ? (int64_t)kt * kBK : 0;
-        // bounds from the tile's first column: the last row's bytes end with the tile's columns
-        const i32x4 p = buffer(w.P + r * w.ldp, left > 0 ? (left - 1) * w.ldp * 2 + w.rows * 2 : 0);
-        const i32x4 q = buffer(w.Q + r * w.N, left > 0 ? (left - 1) * w.N * 2 + w.cols * 2 : 0);
+    // Where the requests have got to: the next stage's rows of the tile they are in.  Bounds go to the tile's last
+    // column in the last row.
+    const char *rp, *rq;
+    int ldp2, ldq2, rows2, cols2, left;  // bytes; rows left
+    uint32_t vp[kOps], vq[kOps];
+    auto start = [&](const WeightTile &w) {
+        rp = (const char *)w.P, rq = (const char *)w.Q;
+        ldp2 = w.ldp * 2, ldq2 = w.N * 2, rows2 = w.rows * 2, cols2 = w.cols * 2, left = w.count;
 #pragma unroll
         for (int i = 0; i < kOps; ++i) {
-            dma(p, (uint32_t)(sr[i] * w.ldp * 2 + sc[i]), 0, dst + i * 1024);
-            dma(q, (uint32_t)(sr[i] * w.N * 2 + sc[i]), 0, dst + kHalf + i * 1024);
+            vp[i] = (uint32_t)(sr[i] * ldp2 + sc[i]);
+            vq[i] = (uint32_t)(sr[i] * ldq2 + sc[i]);
         }
+    };
+    auto request = [&](int slot) {
+        const uint32_t dst = lds0 + slot * kStage;
+        const int n = min(kBK, left);
+        const i32x4 p = buffer(rp, n > 0 ? (n - 1) * ldp2 + rows2 : 0), q = buffer(rq, n > 0 ? (n - 1) * ldq2 + cols2 : 0);
+#pragma unroll
+        for (int i = 0; i < kOps; ++i) {
+            dma(p, vp[i], 0, dst + i * 1024);
+            dma(q, vq[i], 0, dst + kHalf + i * 1024);
+        }
+        rp += (int64_t)kBK * ldp2;
+        rq += (int64_t)kBK * ldq2;
+        left -= kBK;
     };
 
     bf16x8 fq[2][2], fp[2][4];
@@ -446,11 +463,12 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
     WeightTile next = weight_tile(a, wt, weight_tile_index(wt, block, 1));
     if (!cur.live) return;
     int base = 0;  // ring slot of the tile's place 0
-    auto place = [&](int n, int L, int slot) {  // requests place n of the current tile
-        if (n < L) request(cur, n, slot);
-        else request(next, n - L, slot);
+    auto place = [&](int n, int L, int slot) {  // requests place n of the current tile; in order
+        if (n == L) start(next);
+        request(slot);
     };
-    for (int n = 0; n < 4; ++n) place(n, max(cur.nk, 4), n);
+    start(cur);
+    for (int n = 0; n < 4; ++n) request(n);
     while (true) {
         const int nk = cur.nk, L = max(nk, 4);
         place(4, L, ring(base + 4));
