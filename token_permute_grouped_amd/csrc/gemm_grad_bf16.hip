@@ -284,10 +284,29 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
     lds_barrier();
     if constexpr (kKind == Grad::kGlu) {
         // dh goes through LDS in fp32, 128 columns at a time (wave columns 0, 1, then 2, 3): a row of
-        // 32 chunks of 4 values, chunk c of row r at c ^ (r & 31).  A thread then takes 8 columns of a
-        // row: reads gate and up, writes both gradients and h, each 16 bytes.
+        // 32 chunks of 4 values, chunk c of row r at c ^ (r & 31).  A thread then takes 8 columns of
+        // eight rows: reads gate and up (three rows ahead), writes both gradients and h, each 16 bytes.  Buffer
+        // bounds keep rows past the live ones and columns past N out.
+        const int bytes = live * N * 2;
+        const __amdgpu_buffer_rsrc_t rG = row_rsrc((void *)(a.gu + (row0 + m0) * 2 * N), 2 * bytes);
+        const __amdgpu_buffer_rsrc_t rD = row_rsrc(a.dgu + (row0 + m0) * 2 * N, 2 * bytes);
+        const __amdgpu_buffer_rsrc_t rH = row_rsrc(C + (row0 + m0) * N, bytes);
+        const int c8 = tid & 15, r16 = tid >> 4;  // 8-column group and first row of this thread
+        constexpr int kAhead = 3, kStep = kThreads / 16;
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
+            const int col = n0 + p * 128 + c8 * 8;  // hidden column
+            const int gcol = a.il == 0 ? col : col / a.il * 2 * a.il + col % a.il;
+            const uint32_t up = (a.il == 0 ? N : a.il) * 2;
+            const uint32_t out = col < N ? 0u : 0x80000000u;
+            u32x4 gv[kAhead], uv[kAhead];
+            auto load_gu = [&](int i, int tr) {
+                const uint32_t o = out + (uint32_t)(tr * 2 * N + gcol) * 2u;
+                gv[i] = __builtin_amdgcn_raw_buffer_load_b128(rG, o, 0, 0);
+                uv[i] = __builtin_amdgcn_raw_buffer_load_b128(rG, o + up, 0, 0);
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load_gu(i, r16 + i * kStep);
             if ((wn >> 1) == p) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
@@ -304,27 +323,25 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
                 }
             }
             lds_barrier();
-            const int c8 = tid & 15;                       // 8-column group of this thread
-            const int col = n0 + p * 128 + c8 * 8;         // hidden column
-            const int gcol = a.il == 0 ? col : col / a.il * 2 * a.il + col % a.il, ucol = gcol + (a.il == 0 ? N : a.il);
-            if (col < N) {
-                for (int tr = tid >> 4; tr < live; tr += kThreads / 16) {
-                    const int64_t r = row0 + m0 + tr;
-                    const u32x4 gv = *(const u32x4 *)(a.gu + r * 2 * N + gcol);
-                    const u32x4 uv = *(const u32x4 *)(a.gu + r * 2 * N + ucol);
-                    const f32x4 d0 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2) ^ (tr & 31)) << 4));
-                    const f32x4 d1 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2 + 1) ^ (tr & 31)) << 4));
-                    float dg[8], du[8], hv[8];
+#pragma unroll 1
+            for (int tr = r16; tr < live; tr += kStep) {
+                const f32x4 d0 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2) ^ (tr & 31)) << 4));
+                const f32x4 d1 = *(const f32x4 *)(lds + tr * 512 + (((c8 * 2 + 1) ^ (tr & 31)) << 4));
+                const u32x4 g4 = gv[0], u4 = uv[0];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float g = __uint_as_float(q & 1 ? gv[q >> 1] & 0xffff0000u : gv[q >> 1] << 16);
-                        const float u = __uint_as_float(q & 1 ? uv[q >> 1] & 0xffff0000u : uv[q >> 1] << 16);
-                        glu_grad(g, u, q < 4 ? d0[q & 3] : d1[q & 3], a.clamp, dg[q], du[q], hv[q]);
-                    }
-                    *(u32x4 *)(a.dgu + r * 2 * N + gcol) = pack8(dg);
-                    *(u32x4 *)(a.dgu + r * 2 * N + ucol) = pack8(du);
-                    *(u32x4 *)(C + r * N + col) = pack8(hv);
+                for (int i = 0; i + 1 < kAhead; ++i) gv[i] = gv[i + 1], uv[i] = uv[i + 1];
+                load_gu(kAhead - 1, tr + kAhead * kStep);
+                float dg[8], du[8], hv[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float g = __uint_as_float(q & 1 ? g4[q >> 1] & 0xffff0000u : g4[q >> 1] << 16);
+                    const float u = __uint_as_float(q & 1 ? u4[q >> 1] & 0xffff0000u : u4[q >> 1] << 16);
+                    glu_grad(g, u, q < 4 ? d0[q & 3] : d1[q & 3], a.clamp, dg[q], du[q], hv[q]);
                 }
+                const uint32_t o = out + (uint32_t)(tr * 2 * N + gcol) * 2u;
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(dg), rD, o, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(du), rD, o + up, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(hv), rH, out + (uint32_t)(tr * N + col) * 2u, 0, 0);
             }
             lds_barrier();
         }
