@@ -59,11 +59,16 @@ def test_route_topk_backward_ties_go_to_the_lower_expert():
 
 # ------------------------------------------------------------------------------------------------ grouped FFN
 class Ffn:
-    """rows of experts with the given counts, spare rows behind them full of NaN"""
+    """rows of experts with the given counts, spare rows behind them full of NaN (one row is always spare where the
+    bound on the tiles, S / 256 + min(E, S), has to pass 256)"""
 
-    def __init__(self, counts, H, I, il=0, clamp=0.0, spare=3, seed=0, scale=1.0):
+    def __init__(self, counts, H, I, il=0, clamp=0.0, spare=3, seed=0, scale=1.0, experts=0):
+        """experts: as many in all, those behind `counts` without rows"""
         g = _gen(seed + H + I)
+        self.live_experts = len(counts)
+        counts = counts + [0] * (experts - len(counts))
         E, R = len(counts), sum(counts)
+        spare = max(spare, experts + 1 - R)
         self.counts, self.H, self.I, self.il, self.clamp, self.R, self.S = counts, H, I, il, clamp, R, R + spare
         self.off = [sum(counts[:e]) for e in range(E + 1)]
         self.p = tpg.make_problem(R + spare, H, I, E, 1, tpg.MOE_PREC_BF16, il, clamp)
@@ -86,7 +91,7 @@ class Ffn:
 
     def reference(self):
         """(value, slack) of dx, dw1, dw2 by autograd of the fp64 forward"""
-        E, H, I = len(self.counts), self.H, self.I
+        E, H, I = self.live_experts, self.H, self.I
         dx, dxs = torch.zeros(self.R, H, dtype=torch.float64), torch.zeros(self.R, H, dtype=torch.float64)
         dw1, dw1s = (torch.zeros(E, 2 * I, H, dtype=torch.float64) for _ in range(2))
         dw2, dw2s = (torch.zeros(E, H, I, dtype=torch.float64) for _ in range(2))
@@ -124,6 +129,9 @@ class Ffn:
             if what == "dx":
                 assert torch.isnan(got[R:]).all()  # rows behind the last one stay
                 got = got[:R]
+            else:
+                assert (got[self.live_experts:] == 0).all()
+                got = got[:self.live_experts]
             close(got, ref, slack, what)
 
 
@@ -140,12 +148,16 @@ FFN_CASES = {
     "long": dict(counts=[2000], H=256, I=256),
     "wide": dict(counts=[70, 3], H=1152, I=640),
     "large_values": dict(counts=[50, 20], H=128, I=128, scale=60.0),
+    "long_ragged": dict(counts=[1, 900, 129, 127], H=384, I=128, il=32),
 }
 
 
+@pytest.mark.parametrize("experts", [0, 256])
 @pytest.mark.parametrize("name", FFN_CASES)
-def test_grouped_ffn_backward(name):
-    f = Ffn(**FFN_CASES[name])
+def test_grouped_ffn_backward(name, experts):
+    """a small layer takes tiles of 128; with 256 experts (most of them empty) the bound on its tiles is above what
+    fits the chip, and it takes tiles of 256"""
+    f = Ffn(**FFN_CASES[name], experts=experts)
     f.check(f.backward())
 
 

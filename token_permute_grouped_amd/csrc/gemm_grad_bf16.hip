@@ -43,15 +43,25 @@
 namespace tpg {
 
 namespace {
-constexpr int kBM = kGemmBM, kBN = 256, kBK = 32;
-constexpr int kWaves = 8, kThreads = 64 * kWaves, kWaveN = 4;
-constexpr int kHalf = kBK * 512;             // 16 KB: one operand of a stage
-constexpr int kStage = 2 * kHalf;            // P, then Q
+constexpr int kBK = 32;
+constexpr int kWaves = 8, kThreads = 64 * kWaves, kWaveN = 4;  // 2 x 4 waves
 constexpr int kStages = 5;
-constexpr int kOps = kHalf / 1024 / kWaves;  // DMAs per wave, stage and operand (2)
-static_assert(kBM * kBK * 2 == kHalf && kBN * 2 == 512, "both operand layouts fill the same 16 KB");
+
+// A TM x TM tile (256, or 128 for layers with too few tiles of 256 for the chip)
+template <int TM>
+struct Shape {
+    static constexpr int kRows = TM / 2, kCols = TM / kWaveN;      // of a wave
+    static constexpr int kNB = kRows / 32, kNX = kCols / 32;       // its 32 x 32 blocks
+    static constexpr int kHalf = TM * kBK * 2;                     // bytes of one operand's stage, in either layout
+    static constexpr int kStage = 2 * kHalf;                       // P, then Q
+    static constexpr int kOps = kHalf / 1024 / kWaves;             // DMAs per wave, stage and operand
+    static constexpr int kChunks = TM / 8, kLines = 64 / kChunks;  // 16-byte chunks of a row; rows a wave's access covers
+    static constexpr int kLds = kStages * kStage;                  // 160 KB: one workgroup per CU; 80 KB: two
+};
 
 enum class Grad { kGlu, kIn };
+
+constexpr int64_t kSmallTiles = 256;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -81,13 +91,14 @@ __device__ __forceinline__ int tchunk(int r, int p) { return p ^ ((r & 3) << 2);
 // MFMA fragment of 32 columns n0.. and the 16 k of step ks: lane l gets column n0 + (l & 31), k = 16 ks +
 // 8 (l >> 5) + 0..7, by two transposing reads of 4 k each.  In one, lane i of a group of 16 names 4
 // columns (i & 3) of row i >> 2 and gets column i of the 4 rows.
+template <int TM>
 __device__ __forceinline__ bf16x8 load_trans(const unsigned char *stage, int n0, int ks, int lane) {
     const int r = (lane & 15) >> 2, seg = (n0 >> 4) + ((lane >> 4) & 1);
     const unsigned char *p =
-        stage + (ks * 16 + (lane >> 5) * 8 + r) * 512 + ((seg ^ (2 * r)) << 5) + (lane & 3) * 8;
+        stage + (ks * 16 + (lane >> 5) * 8 + r) * (TM * 2) + ((seg ^ (2 * r)) << 5) + (lane & 3) * 8;
     typedef __attribute__((address_space(3))) bf16x4 *lds_ptr;
     const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)p);
-    const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(p + 4 * 512));
+    const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(p + 4 * TM * 2));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -129,12 +140,14 @@ struct WeightTiles {
     int n1, per_expert, total, run, blocks;  // n1: dW1's tiles of an expert; per_expert: both matrices'
 };
 __host__ __device__ inline int blocks_of(int n, int size) { return (n + size - 1) / size; }
+template <int TM>
 __host__ __device__ inline WeightTiles weight_tiles(int E, bool dw1, bool dw2, int H, int I) {
     WeightTiles t;
-    t.n1 = dw1 ? blocks_of(2 * I, kBM) * blocks_of(H, kBN) : 0;
-    t.per_expert = t.n1 + (dw2 ? blocks_of(H, kBM) * blocks_of(I, kBN) : 0);
+    t.n1 = dw1 ? blocks_of(2 * I, TM) * blocks_of(H, TM) : 0;
+    t.per_expert = t.n1 + (dw2 ? blocks_of(H, TM) * blocks_of(I, TM) : 0);
     t.total = E * t.per_expert;
-    t.run = t.total >= 256 ? 32 : (t.total + 7) / 8;
+    const int resident = TM == 256 ? 256 : 512;  // workgroups
+    t.run = t.total >= resident ? resident / 8 : (t.total + 7) / 8;
     t.blocks = 8 * t.run;
     return t;
 }
@@ -147,13 +160,13 @@ __device__ __forceinline__ int weight_tile_index(const WeightTiles &t, int block
 
 // What the products need to know of the offsets, in one workgroup of 256: the m-tile list, and
 // order[rank] = {expert, first row, rows}, by descending row count (ties: lower expert first).
-__global__ __launch_bounds__(256) void grad_prepare_kernel(const int32_t *__restrict__ offsets, int E,
+__global__ __launch_bounds__(256) void grad_prepare_kernel(const int32_t *__restrict__ offsets, int E, int bm,
                                                            int32_t *__restrict__ tiles, int32_t *__restrict__ n_tiles,
                                                            int4 *__restrict__ order) {
     __shared__ int cnt[256], ws[8];
     const int e = threadIdx.x;
     cnt[e] = e < E ? offsets[e + 1] - offsets[e] : -1;
-    build_tile_list(offsets, E, kBM, 0, tiles, n_tiles, ws);  // holds a barrier
+    build_tile_list(offsets, E, bm, 0, tiles, n_tiles, ws);  // holds a barrier
     if (e >= E) return;
     int rank = 0;
     for (int i = 0; i < E; ++i) rank += cnt[i] > cnt[e] || (cnt[i] == cnt[e] && i < e);
@@ -172,20 +185,21 @@ struct GradArgs {
     float clamp;
 };
 
-// One tile of GradGlu or GradIn; lds: kStages * kStage.
-template <Grad kKind>
+// One tile of GradGlu or GradIn.
+template <Grad kKind, int TM>
 __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsigned char *lds) {
+    using S = Shape<TM>;
     // ---- operands P [S][K], Q [E][K][N], C [S][N]; tile: rows m0.. of expert e, columns n0..
     const uint16_t *P = kKind == Grad::kGlu ? a.dy : a.dgu, *Q = kKind == Grad::kGlu ? a.w2 : a.w1;
     uint16_t *C = kKind == Grad::kGlu ? a.h : a.dx;
     const int K = kKind == Grad::kGlu ? a.H : 2 * a.I, N = kKind == Grad::kGlu ? a.I : a.H;
     int mt, nt;
-    if (!row_tile(block, blocks_of(N, kBN), a.n_tiles, mt, nt)) return;
+    if (!row_tile(block, blocks_of(N, TM), a.n_tiles, mt, nt)) return;
     const int e = __builtin_amdgcn_readfirstlane(a.tiles[2 * mt]);
-    const int m0 = __builtin_amdgcn_readfirstlane(a.tiles[2 * mt + 1]), n0 = nt * kBN;
+    const int m0 = __builtin_amdgcn_readfirstlane(a.tiles[2 * mt + 1]), n0 = nt * TM;
     const int64_t row0 = __builtin_amdgcn_readfirstlane(a.offsets[e]);
     const int count = __builtin_amdgcn_readfirstlane(a.offsets[e + 1]) - (int)row0;
-    const int live = min(kBM, count - m0);  // live rows of the tile
+    const int live = min(TM, count - m0);  // live rows of the tile
     const int nk = K / kBK;
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -194,25 +208,26 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
     const int half = lane >> 5;
 
     // ---- DMAs of a stage: byte offsets of this lane's 16 bytes
-    uint32_t offP[kOps], offQ[kOps];
+    uint32_t offP[S::kOps], offQ[S::kOps];
 #pragma unroll
-    for (int i = 0; i < kOps; ++i) {
-        const int r = wave * (kBK / kWaves) + i * 2 + half, c = tchunk(r, lane & 31) * 8;  // stage row, column
+    for (int i = 0; i < S::kOps; ++i) {
+        const int r = wave * (kBK / kWaves) + i * S::kLines + lane / S::kChunks;  // stage row
+        const int c = tchunk(r, lane % S::kChunks) * 8;                           // column
         // columns past N are not read (the last row's would lie behind the matrix)
         offQ[i] = n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
-        const int pr = wave * (kBM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
+        const int pr = wave * (TM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
         offP[i] = pr < live ? (uint32_t)(pr * K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
     }
-    const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
+    const uint32_t lds0 = lds_address(lds) + wave * (S::kOps * 1024);
     i32x4 rp = buffer(P + (row0 + m0) * K, live * K * 2), rq = buffer(Q + (int64_t)e * K * N, K * N * 2);
     int sp = 0, sq = 0, left = nk;  // the next stage's offsets in P's rows and in Q, and stages left
     auto request = [&](int slot) {
-        const uint32_t dst = lds0 + slot * kStage;
+        const uint32_t dst = lds0 + slot * S::kStage;
         if (left == 0) rp.z = rq.z = 0;  // behind the last stage: out of bounds, nothing is read
 #pragma unroll
-        for (int i = 0; i < kOps; ++i) {
+        for (int i = 0; i < S::kOps; ++i) {
             dma(rp, offP[i], sp, dst + i * 1024);
-            dma(rq, offQ[i], sq, dst + kHalf + i * 1024);
+            dma(rq, offQ[i], sq, dst + S::kHalf + i * 1024);
         }
         if (--left > 0) {
             sp += kBK * 2;
@@ -220,35 +235,35 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
         }
     };
 
-    f32x16 acc[2][4];
+    f32x16 acc[S::kNX][S::kNB];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < S::kNX; ++x)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < S::kNB; ++b)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[x][b][v] = 0.f;
 
     // NB: 32-row blocks of this wave with a live row
     auto mainloop = [&](auto nb_tag) {
         constexpr int NB = decltype(nb_tag)::value;
-        constexpr int NR = NB + 4, NM = 2 * NB;  // LDS reads and MFMAs of a step
-        constexpr int G = 2 * kOps;                            // DMAs of a stage
-        bf16x8 fq[2][2], fp[2][NB > 0 ? NB : 1];
+        constexpr int NR = NB + 2 * S::kNX, NM = S::kNX * NB;  // LDS reads and MFMAs of a step
+        constexpr int G = 2 * S::kOps;                            // DMAs of a stage
+        bf16x8 fq[2][S::kNX], fp[2][NB > 0 ? NB : 1];
         auto load = [&](int buf, int slot, int ks) {
             if constexpr (NB > 0) {
-                const unsigned char *s = lds + slot * kStage;
+                const unsigned char *s = lds + slot * S::kStage;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) fq[buf][x] = load_trans(s + kHalf, wn * 64 + x * 32, ks, lane);
+                for (int x = 0; x < S::kNX; ++x) fq[buf][x] = load_trans<TM>(s + S::kHalf, wn * S::kCols + x * 32, ks, lane);
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    fp[buf][b] = load_rows(s, wm * 128 + b * 32, ks, lane);
+                    fp[buf][b] = load_rows(s, wm * S::kRows + b * 32, ks, lane);
             }
         };
         auto mfmas = [&](int buf) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < S::kNX; ++x)
                     acc[x][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[buf][x], fp[buf][b], acc[x][b], 0, 0, 0);
         };
 #pragma unroll
@@ -271,19 +286,20 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
         }
         wait_vmcnt<0>();  // the LDS is written again below
     };
-    switch (max(0, min(4, (live - wm * 128 + 31) >> 5))) {
-        case 4: mainloop(std::integral_constant<int, 4>{}); break;
-        case 3: mainloop(std::integral_constant<int, 3>{}); break;
+    const int nb_live = max(0, min(S::kNB, (live - wm * S::kRows + 31) >> 5));
+    switch (nb_live) {
+        case 4: if constexpr (S::kNB == 4) mainloop(std::integral_constant<int, 4>{}); break;
+        case 3: if constexpr (S::kNB == 4) mainloop(std::integral_constant<int, 3>{}); break;
         case 2: mainloop(std::integral_constant<int, 2>{}); break;
         case 1: mainloop(std::integral_constant<int, 1>{}); break;
         default: mainloop(std::integral_constant<int, 0>{}); break;
     }
 
-    // ---- epilogue: lane holds tile row wm 128 + b 32 + (lane & 31) and columns wn 64 + x 32 + 8 (v >> 2) +
-    //      4 (lane >> 5) + (v & 3).  The tile goes through LDS, so that whole rows are read and stored.
+    // ---- epilogue: lane holds row wm kRows + b 32 + (lane & 31) and columns wn kCols + x 32 + 8 (v >>
+    //      2) + 4 (lane >> 5) + (v & 3).  The tile goes through LDS, so that whole rows are read and stored.
     lds_barrier();
     if constexpr (kKind == Grad::kGlu) {
-        // dh goes through LDS in fp32, 128 columns at a time (wave columns 0, 1, then 2, 3): a row of
+        // dh goes through LDS in fp32, 128 columns at a time: a row of
         // 32 chunks of 4 values, chunk c of row r at c ^ (r & 31).  A thread then takes 8 columns of
         // eight rows: reads gate and up (three rows ahead), writes both gradients and h, each 16 bytes.  Buffer
         // bounds keep rows past the live ones and columns past N out.
@@ -294,7 +310,7 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
         const int c8 = tid & 15, r16 = tid >> 4;  // 8-column group and first row of this thread
         constexpr int kAhead = 3, kStep = kThreads / 16;
 #pragma unroll 1
-        for (int p = 0; p < 2; ++p) {
+        for (int p = 0; p < TM / 128; ++p) {
             const int col = n0 + p * 128 + c8 * 8;  // hidden column
             const int gcol = a.il == 0 ? col : col / a.il * 2 * a.il + col % a.il;
             const uint32_t up = (a.il == 0 ? N : a.il) * 2;
@@ -307,15 +323,15 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) load_gu(i, r16 + i * kStep);
-            if ((wn >> 1) == p) {
+            if ((wn * S::kCols) / 128 == p) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int tr = wm * 128 + b * 32 + (lane & 31);
+                for (int b = 0; b < S::kNB; ++b) {
+                    const int tr = wm * S::kRows + b * 32 + (lane & 31);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
+                    for (int x = 0; x < S::kNX; ++x)
 #pragma unroll
                         for (int g4 = 0; g4 < 4; ++g4) {
-                            const int c = (wn & 1) * 16 + x * 8 + g4 * 2 + half;
+                            const int c = (wn * S::kCols) % 128 / 4 + x * 8 + g4 * 2 + half;
                             *(f32x4 *)(lds + tr * 512 + ((c ^ (tr & 31)) << 4)) =
                                 (f32x4){acc[x][b][g4 * 4], acc[x][b][g4 * 4 + 1], acc[x][b][g4 * 4 + 2],
                                         acc[x][b][g4 * 4 + 3]};
@@ -347,27 +363,27 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
         }
         return;
     }
-    auto cofs = [](int r, int c) { return r * (kBN * 2) + ((c ^ (r & 15)) << 4); };
+    auto cofs = [](int r, int c) { return r * (TM * 2) + ((c ^ (r & 15)) << 4); };
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const int tr = wm * 128 + b * 32 + (lane & 31);
+    for (int b = 0; b < S::kNB; ++b) {
+        const int tr = wm * S::kRows + b * 32 + (lane & 31);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < S::kNX; ++x)
 #pragma unroll
             for (int g4 = 0; g4 < 4; ++g4) {
                 u32x2 o;
                 o.x = pack_bf16x2(acc[x][b][g4 * 4 + 0], acc[x][b][g4 * 4 + 1]);
                 o.y = pack_bf16x2(acc[x][b][g4 * 4 + 2], acc[x][b][g4 * 4 + 3]);
-                *(u32x2 *)(lds + cofs(tr, wn * 8 + x * 4 + g4) + half * 8) = o;
+                *(u32x2 *)(lds + cofs(tr, wn * (S::kCols / 8) + x * 4 + g4) + half * 8) = o;
             }
     }
     lds_barrier();
-    const int c = n0 + (lane & 31) * 8;
+    const int ch = lane % S::kChunks, c = n0 + ch * 8;
     if (c < N) {
         uint16_t *out = C + (row0 + m0) * N + c;
 #pragma unroll 4
-        for (int tr = wave * 2 + half; tr < kBM; tr += kWaves * 2)
-            if (tr < live) *(u32x4 *)(out + (int64_t)tr * N) = *(const u32x4 *)(lds + cofs(tr, lane & 31));
+        for (int tr = wave * S::kLines + lane / S::kChunks; tr < TM; tr += kWaves * S::kLines)
+            if (tr < live) *(u32x4 *)(out + (int64_t)tr * N) = *(const u32x4 *)(lds + cofs(tr, ch));
     }
 }
 
@@ -380,6 +396,7 @@ struct WeightTile {
     int nk;                 // stages
     bool live;
 };
+template <int TM>
 __device__ __forceinline__ WeightTile weight_tile(const GradArgs &a, const WeightTiles &wt, int g) {
     WeightTile w = {};
     w.live = g < wt.total;
@@ -391,9 +408,9 @@ __device__ __forceinline__ WeightTile weight_tile(const GradArgs &a, const Weigh
     if (!first) t -= wt.n1;
     w.ldp = first ? 2 * a.I : a.H;
     w.N = first ? a.H : a.I;
-    const int nb_m = blocks_of(w.ldp, kBM), nb_n = blocks_of(w.N, kBN);
+    const int nb_m = blocks_of(w.ldp, TM), nb_n = blocks_of(w.N, TM);
     const int band = t / (kBand * nb_n), rows = min(kBand, nb_m - band * kBand), r = t - band * kBand * nb_n;
-    const int m0 = (band * kBand + r % rows) * kBM, n0 = r / rows * kBN;
+    const int m0 = (band * kBand + r % rows) * TM, n0 = r / rows * TM;
     const int e = __builtin_amdgcn_readfirstlane(o.x);
     const int64_t row0 = __builtin_amdgcn_readfirstlane(o.y);
     w.count = __builtin_amdgcn_readfirstlane(o.z);
@@ -401,12 +418,12 @@ __device__ __forceinline__ WeightTile weight_tile(const GradArgs &a, const Weigh
     w.P = (first ? a.dgu : a.dy) + row0 * w.ldp + m0;
     w.Q = (first ? a.x : a.h) + row0 * w.N + n0;
     w.C = (first ? a.dw1 : a.dw2) + ((int64_t)e * w.ldp + m0) * w.N + n0;
-    w.rows = min(kBM, w.ldp - m0);
-    w.cols = min(kBN, w.N - n0);
+    w.rows = min(TM, w.ldp - m0);
+    w.cols = min(TM, w.N - n0);
     return w;
 }
 
-// The weight gradients' tiles of one workgroup, one after the other; lds: kStages * kStage.
+// The weight gradients' tiles of one workgroup, one after the other.
 //
 // The ring runs on from one tile to the next: while a tile's last stages are multiplied, the first four of the next
 // are requested, so its data is there when the tile has been stored.  A tile takes L = max(nk, 4) places of the
@@ -414,70 +431,73 @@ __device__ __forceinline__ WeightTile weight_tile(const GradArgs &a, const Weigh
 // tile's n - L, and place L + 4 stays free until the tile has gone through it to memory, 64 rows at a time.
 // Waiting for fewer than n outstanding requests is right whatever the stores do: they only make the count larger.
 // (One tile per workgroup, with the whole ring filled and drained for each: 8 us more per tile.)
+template <int TM>
 __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, unsigned char *lds) {
-    const WeightTiles wt = weight_tiles(a.E, a.dw1 != nullptr, a.dw2 != nullptr, a.H, a.I);
+    using S = Shape<TM>;
+    const WeightTiles wt = weight_tiles<TM>(a.E, a.dw1 != nullptr, a.dw2 != nullptr, a.H, a.I);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / kWaveN, wn = wave % kWaveN;
     const int half = lane >> 5;
-    constexpr int G = 2 * kOps;  // DMAs of a stage
+    constexpr int G = 2 * S::kOps;  // DMAs of a stage
 
-    int sr[kOps], sc[kOps];  // stage row and column byte of this lane's DMAs
+    int sr[S::kOps], sc[S::kOps];  // stage row and column byte of this lane's DMAs
 #pragma unroll
-    for (int i = 0; i < kOps; ++i) {
-        sr[i] = wave * (kBK / kWaves) + i * 2 + half;
-        sc[i] = tchunk(sr[i], lane & 31) * 16;
+    for (int i = 0; i < S::kOps; ++i) {
+        sr[i] = wave * (kBK / kWaves) + i * S::kLines + lane / S::kChunks;
+        sc[i] = tchunk(sr[i], lane % S::kChunks) * 16;
     }
-    const uint32_t lds0 = lds_address(lds) + wave * (kOps * 1024);
+    const uint32_t lds0 = lds_address(lds) + wave * (S::kOps * 1024);
     // Where the requests have got to: the next stage's rows of the tile they are in.  Bounds go to the tile's last
     // column in the last row.
     const char *rp, *rq;
     int ldp2, ldq2, rows2, cols2, left;  // bytes; rows left
-    uint32_t vp[kOps], vq[kOps];
+    uint32_t vp[S::kOps], vq[S::kOps];
     auto start = [&](const WeightTile &w) {
         rp = (const char *)w.P, rq = (const char *)w.Q;
         ldp2 = w.ldp * 2, ldq2 = w.N * 2, rows2 = w.rows * 2, cols2 = w.cols * 2, left = w.count;
 #pragma unroll
-        for (int i = 0; i < kOps; ++i) {
+        for (int i = 0; i < S::kOps; ++i) {
             vp[i] = (uint32_t)(sr[i] * ldp2 + sc[i]);
             vq[i] = (uint32_t)(sr[i] * ldq2 + sc[i]);
         }
     };
     auto request = [&](int slot) {
-        const uint32_t dst = lds0 + slot * kStage;
+        const uint32_t dst = lds0 + slot * S::kStage;
         const int n = min(kBK, left);
         const i32x4 p = buffer(rp, n > 0 ? (n - 1) * ldp2 + rows2 : 0), q = buffer(rq, n > 0 ? (n - 1) * ldq2 + cols2 : 0);
 #pragma unroll
-        for (int i = 0; i < kOps; ++i) {
+        for (int i = 0; i < S::kOps; ++i) {
             dma(p, vp[i], 0, dst + i * 1024);
-            dma(q, vq[i], 0, dst + kHalf + i * 1024);
+            dma(q, vq[i], 0, dst + S::kHalf + i * 1024);
         }
         rp += (int64_t)kBK * ldp2;
         rq += (int64_t)kBK * ldq2;
         left -= kBK;
     };
 
-    bf16x8 fq[2][2], fp[2][4];
-    f32x16 acc[2][4];
+    constexpr int NR = 2 * (S::kNX + S::kNB), NM = S::kNX * S::kNB;  // LDS reads and MFMAs of a step
+    bf16x8 fq[2][S::kNX], fp[2][S::kNB];
+    f32x16 acc[S::kNX][S::kNB];
     auto load = [&](int buf, int slot, int ks) {
-        const unsigned char *s = lds + slot * kStage;
+        const unsigned char *s = lds + slot * S::kStage;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) fq[buf][x] = load_trans(s + kHalf, wn * 64 + x * 32, ks, lane);
+        for (int x = 0; x < S::kNX; ++x) fq[buf][x] = load_trans<TM>(s + S::kHalf, wn * S::kCols + x * 32, ks, lane);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) fp[buf][b] = load_trans(s, wm * 128 + b * 32, ks, lane);
+        for (int b = 0; b < S::kNB; ++b) fp[buf][b] = load_trans<TM>(s, wm * S::kRows + b * 32, ks, lane);
     };
     auto mfmas = [&](int buf) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < S::kNB; ++b)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < S::kNX; ++x)
                 acc[x][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[buf][x], fp[buf][b], acc[x][b], 0, 0, 0);
     };
     auto ring = [](int slot) { return slot >= kStages ? slot - kStages : slot; };
 
     int step = 0;
-    WeightTile cur = weight_tile(a, wt, weight_tile_index(wt, block, 0));
-    WeightTile next = weight_tile(a, wt, weight_tile_index(wt, block, 1));
+    WeightTile cur = weight_tile<TM>(a, wt, weight_tile_index(wt, block, 0));
+    WeightTile next = weight_tile<TM>(a, wt, weight_tile_index(wt, block, 1));
     if (!cur.live) return;
     int base = 0;  // ring slot of the tile's place 0
     auto place = [&](int n, int L, int slot) {  // requests place n of the current tile; in order
@@ -490,9 +510,9 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
         const int nk = cur.nk, L = max(nk, 4);
         place(4, L, ring(base + 4));
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < S::kNX; ++x)
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < S::kNB; ++b)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[x][b][v] = 0.f;
         wait_vmcnt<(kStages - 1) * G>();  // place 0 has landed
@@ -503,18 +523,18 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
             for (int kt = 0; kt + 1 < nk; ++kt) {
                 load(1, slot, 1);
                 mfmas(0);
-                interleave_ds_mfma<12, 8>();
+                interleave_ds_mfma<NR, NM>();
                 wait_vmcnt<(kStages - 2) * G>();  // place kt+1 has landed; kt+2 .. kt+4 may be in flight
                 lds_barrier();
                 place(kt + kStages, L, slot);
                 slot = ring(slot + 1);
                 load(0, slot, 0);
                 mfmas(1);
-                interleave_ds_mfma<12, 8>();
+                interleave_ds_mfma<NR, NM>();
             }
             load(1, slot, 1);
             mfmas(0);
-            interleave_ds_mfma<12, 8>();
+            interleave_ds_mfma<NR, NM>();
             mfmas(1);
             slot = ring(slot + 1);
         }
@@ -525,34 +545,35 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
         const int stage_slot = ring(base + 4);  // place L + 4
         const WeightTile done = cur;
         cur = next;
-        next = weight_tile(a, wt, weight_tile_index(wt, block, ++step + 1));
+        next = weight_tile<TM>(a, wt, weight_tile_index(wt, block, ++step + 1));
 
-        // ---- store: a lane holds row wm 128 + b 32 + (lane & 31) and columns wn 64 + x 32 + 8 (v >> 2) + 4 (lane >>
-        //      5) + (v & 3); block row b of both wave rows goes through the free place at a time
+        // ---- store: a lane holds row wm kRows + b 32 + (lane & 31) and columns wn kCols + x 32 + 8 (v >> 2) + 4
+        //      (lane >> 5) + (v & 3); block row b of both wave rows goes through the free place at a time
         wait_vmcnt<(kStages - 1) * G>();  // nothing is on its way to it
-        unsigned char *st = lds + stage_slot * kStage;
-        auto cofs = [](int r, int c) { return r * (kBN * 2) + ((c ^ (r & 15)) << 4); };
+        unsigned char *st = lds + stage_slot * S::kStage;
+        auto cofs = [](int r, int c) { return r * (TM * 2) + ((c ^ (r & 15)) << 4); };
         const int lr = wm * 32 + (lane & 31);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < S::kNB; ++b) {
             lds_barrier();  // every wave is done with the slot
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < S::kNX; ++x)
 #pragma unroll
                 for (int g4 = 0; g4 < 4; ++g4) {
                     u32x2 o;
                     o.x = pack_bf16x2(acc[x][b][g4 * 4 + 0], acc[x][b][g4 * 4 + 1]);
                     o.y = pack_bf16x2(acc[x][b][g4 * 4 + 2], acc[x][b][g4 * 4 + 3]);
-                    *(u32x2 *)(st + cofs(lr, wn * 8 + x * 4 + g4) + half * 8) = o;
+                    *(u32x2 *)(st + cofs(lr, wn * (S::kCols / 8) + x * 4 + g4) + half * 8) = o;
                 }
             lds_barrier();
-            if ((lane & 31) * 8 < done.cols) {
+            const int ch = lane % S::kChunks;
+            if (ch * 8 < done.cols) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = wave * 2 + half + i * 16, row = (r >> 5) * 128 + b * 32 + (r & 31);
+                for (int i = 0; i < 64 / (kWaves * S::kLines); ++i) {
+                    const int r = (i * kWaves + wave) * S::kLines + lane / S::kChunks;
+                    const int row = (r >> 5) * S::kRows + b * 32 + (r & 31);
                     if (row < done.rows)
-                        *(u32x4 *)(done.C + (int64_t)row * done.N + (lane & 31) * 8) =
-                            *(const u32x4 *)(st + cofs(r, lane & 31));
+                        *(u32x4 *)(done.C + (int64_t)row * done.N + ch * 8) = *(const u32x4 *)(st + cofs(r, ch));
                 }
             }
         }
@@ -562,27 +583,45 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
     wait_vmcnt<0>();  // requests still write to this workgroup's LDS
 }
 
-// GradGlu
-__global__ __launch_bounds__(kThreads, 1) void grad_glu_kernel(GradArgs a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];  // 160 KB
-    grad_row_tile<Grad::kGlu>(a, blockIdx.x, lds);
+// waves per SIMD: two workgroups of the small tiles share a CU
+constexpr int waves_per_simd(int TM) { return TM == 256 ? 2 : 4; }
+
+template <int TM>
+__global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_glu_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<TM>::kLds];
+    grad_row_tile<Grad::kGlu, TM>(a, blockIdx.x, lds);
 }
 
 // GradIn (the first in_blocks workgroups) and GradWeight, which all need GradGlu's results only: in one launch
 // the small layers pay one launch's latency for three, and the large ones fill one product's last round of
 // workgroups with the next one's tiles (the weight gradients' smallest tiles come last).
-__global__ __launch_bounds__(kThreads, 1) void grad_products_kernel(GradArgs a, int in_blocks) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages * kStage];
+template <int TM>
+__global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_products_kernel(GradArgs a, int in_blocks) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<TM>::kLds];
     if ((int)blockIdx.x < in_blocks)
-        grad_row_tile<Grad::kIn>(a, blockIdx.x, lds);
+        grad_row_tile<Grad::kIn, TM>(a, blockIdx.x, lds);
     else
-        grad_weight_tiles(a, blockIdx.x - in_blocks, lds);
+        grad_weight_tiles<TM>(a, blockIdx.x - in_blocks, lds);
 }
 
 namespace {
-int64_t row_blocks(int64_t max_tiles, int N) {
-    const TileMap tm = tile_map(blocks_of(N, kBN));
+int64_t row_blocks(int64_t max_tiles, int nb_n) {
+    const TileMap tm = tile_map(nb_n);
     return (max_tiles + tm.gm - 1) / tm.gm * tm.per_band;
+}
+
+template <int TM>
+hipError_t launch(const GradArgs &a, const moe_problem &p, int32_t *tiles, int32_t *n_tiles, int4 *order, hipStream_t s) {
+    const int64_t max_tiles = grad_max_tiles(p, TM);
+    hipLaunchKernelGGL(grad_prepare_kernel, dim3(1), dim3(256), 0, s, a.offsets, p.E, TM, tiles, n_tiles, order);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(grad_glu_kernel<TM>, dim3(row_blocks(max_tiles, blocks_of(p.I, TM))), dim3(kThreads), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t in_blocks = a.dx ? row_blocks(max_tiles, blocks_of(p.H, TM)) : 0;
+    const WeightTiles wt = weight_tiles<TM>(p.E, a.dw1 != nullptr, a.dw2 != nullptr, p.H, p.I);
+    hipLaunchKernelGGL(grad_products_kernel<TM>, dim3(in_blocks + wt.blocks), dim3(kThreads), 0, s, a, (int)in_blocks);
+    return hipGetLastError();
 }
 }  // namespace
 
@@ -592,16 +631,10 @@ hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const
                                     uint16_t *dw2, hipStream_t s) {
     const GradArgs a = {offsets, tiles, n_tiles, (const int4 *)order, p.E, p.H, p.I, dy, x, (const uint16_t *)w.w1,
                         (const uint16_t *)w.w2, gu, dgu, h, dx, dw1, dw2, p.glu_interleave, p.swiglu_clamp};
-    const int64_t max_tiles = max_m_tiles(p);
-    hipLaunchKernelGGL(grad_prepare_kernel, dim3(1), dim3(256), 0, s, offsets, p.E, tiles, n_tiles, (int4 *)order);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grad_glu_kernel, dim3(row_blocks(max_tiles, p.I)), dim3(kThreads), 0, s, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t in_blocks = dx ? row_blocks(max_tiles, p.H) : 0;
-    const WeightTiles wt = weight_tiles(p.E, dw1 != nullptr, dw2 != nullptr, p.H, p.I);
-    hipLaunchKernelGGL(grad_products_kernel, dim3(in_blocks + wt.blocks), dim3(kThreads), 0, s, a, (int)in_blocks);
-    return hipGetLastError();
+    // 256 x 256 tiles unless their number leaves CUs idle
+    if (grad_max_tiles(p, 256) * blocks_of(p.H, 256) > kSmallTiles)
+        return launch<256>(a, p, tiles, n_tiles, (int4 *)order, s);
+    return launch<128>(a, p, tiles, n_tiles, (int4 *)order, s);
 }
 
 }  // namespace tpg

@@ -98,7 +98,7 @@ BackwardLayout backward_layout(const moe_problem &p) {
     const size_t S = (size_t)n_slots(p);
     size_t o = 0;
     L.tiles = o;
-    o = align256(o + (size_t)max_m_tiles(p) * 2 * 4);
+    o = align256(o + (size_t)grad_max_tiles(p, 128) * 2 * 4);
     L.n_tiles = o;
     o = align256(o + 16);
     L.order = o;

@@ -130,6 +130,11 @@ hipError_t launch_gemm2_bf16(const uint16_t *h, const uint16_t *w2, const int32_
                              const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *y_perm,
                              const int32_t *row_dst, hipStream_t s);
 
+// upper bound of the backward pass's m-tiles of bm rows (256, or 128 for small layers), over any routing
+inline int64_t grad_max_tiles(const moe_problem &p, int bm) {
+    const int64_t S = n_slots(p);
+    return S / bm + std::min<int64_t>(p.E, S);
+}
 // The grouped FFN's backward pass: tiles, n_tiles, order [E][4], dgu [S][2I] and h [S][I] are scratch; dx, dw1 and dw2
 // may be NULL
 hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const uint16_t *gu, const int32_t *offsets,
