@@ -93,15 +93,6 @@ static_assert(kSpRows == kLRows, "a sparse stage is the first activation load of
 
 __device__ __forceinline__ int slot(int r, int kc) { return kc ^ ((r & 7) ^ ((r >> 3) & 1)); }
 
-__device__ __forceinline__ float silu_mul(float g, float u, float clamp) {
-    if (clamp > 0.f) {
-        g = fminf(fmaxf(g, -clamp), clamp);
-        u = fminf(fmaxf(u, -clamp), clamp);
-    }
-    // hardware exp2 / reciprocal (about 1 ulp each): far below the bf16 rounding of h
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return pack_bf16x2(a, b);
 }
@@ -503,7 +494,8 @@ hipError_t launch(const uint16_t *A, const int32_t *row_src, int gather_k, int a
 
 hipError_t launch_gemm1_swiglu_bf16(const uint16_t *x_perm, const uint16_t *w1, const int32_t *offsets,
                                     const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
-                                    int glu_interleave, float clamp, uint16_t *h, uint16_t *gu, hipStream_t s) {
+                                    int glu_interleave, float clamp, uint16_t *h, uint16_t *gu,
+                                    hipStream_t s) {
     if (gu)
         return launch<Gemm::kGluKeep>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
                                       glu_interleave, clamp, h, I, nullptr, s, gu);

@@ -38,6 +38,15 @@ __device__ __forceinline__ void interleave_ds_mfma() {
     }
 }
 
+__device__ __forceinline__ float silu_mul(float g, float u, float clamp) {
+    if (clamp > 0.f) {
+        g = fminf(fmaxf(g, -clamp), clamp);
+        u = fminf(fmaxf(u, -clamp), clamp);
+    }
+    // hardware exp2 / reciprocal (about 1 ulp each): far below the bf16 rounding of h
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
 // Workgroup -> tile map.  Workgroup b runs on XCD b % 8.  Bands of tm.gm m-tiles take
 // tm.per_band workgroups each; a band is cut into 8 rectangles (xm rows of m-tiles x xn
 // columns of n-tiles, about 32 tiles each: one per CU of an XCD), and XCD x takes

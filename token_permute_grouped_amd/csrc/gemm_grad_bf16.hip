@@ -44,14 +44,14 @@ namespace tpg {
 
 namespace {
 constexpr int kBK = 32;
-constexpr int kWaves = 8, kThreads = 64 * kWaves, kWaveN = 4;  // 2 x 4 waves
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kStages = 5;
 
 // A TM x TM tile (256, or 128 for layers with too few tiles of 256 for the chip)
-template <int TM>
+template <int TM, int WN = 4>  // WN: waves along the columns
 struct Shape {
-    static constexpr int kRows = TM / 2, kCols = TM / kWaveN;      // of a wave
-    static constexpr int kNB = kRows / 32, kNX = kCols / 32;       // its 32 x 32 blocks
+    static constexpr int kRows = TM / (kWaves / WN), kCols = TM / WN;  // of a wave
+    static constexpr int kWN = WN, kNB = kRows / 32, kNX = kCols / 32;       // its 32 x 32 blocks
     static constexpr int kHalf = TM * kBK * 2;                     // bytes of one operand's stage, in either layout
     static constexpr int kStage = 2 * kHalf;                       // P, then Q
     static constexpr int kOps = kHalf / 1024 / kWaves;             // DMAs per wave, stage and operand
@@ -59,9 +59,22 @@ struct Shape {
     static constexpr int kLds = kStages * kStage;                  // 160 KB: one workgroup per CU; 80 KB: two
 };
 
-enum class Grad { kGlu, kIn };
+enum class Gemm {
+    kFwdGlu,   // x W1^T -> gu, h
+    kFwdOut,   // h W2^T -> y
+    kGradGlu,  // dy W2 = dh -> dgu, h
+    kGradIn,   // dgu W1 -> dx
+};
+constexpr bool is_forward(Gemm k) { return k == Gemm::kFwdGlu || k == Gemm::kFwdOut; }
 
-constexpr int64_t kSmallTiles = 256;
+// A layer takes 128 x 128 tiles if at most this many tiles of 256 could have work.  Backward pass with 256 / 128: bound
+// 60 (8 experts of 225 rows, H = 896, I = 640) 73 / 46 us, 132 (1 of 8192, 1024, 1024) 214 / 160, 136 (16 of 300, 1024,
+// 1024) 126 / 125, 192 (8 of 512, 2048, 1024) 171 / 169, 296 (16 of 345, 2048, 1408) 294 / 355, 356 (64 of 100, 1024,
+// 512) 138 / 141.
+constexpr int64_t kSmallTiles = 192;
+inline bool small_tiles(const moe_problem &p) {
+    return grad_max_tiles(p, 256) * ((p.H + 255) / 256) <= kSmallTiles;
+}
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -167,7 +180,7 @@ __global__ __launch_bounds__(256) void grad_prepare_kernel(const int32_t *__rest
     const int e = threadIdx.x;
     cnt[e] = e < E ? offsets[e + 1] - offsets[e] : -1;
     build_tile_list(offsets, E, bm, 0, tiles, n_tiles, ws);  // holds a barrier
-    if (e >= E) return;
+    if (e >= E || !order) return;
     int rank = 0;
     for (int i = 0; i < E; ++i) rank += cnt[i] > cnt[e] || (cnt[i] == cnt[e] && i < e);
     order[rank] = make_int4(e, offsets[e], cnt[e], 0);
@@ -179,20 +192,24 @@ struct GradArgs {
     const int4 *order;               // {expert, first row, rows}, most rows first
     int E, H, I;
     const uint16_t *dy, *x, *w1, *w2, *gu;
-    uint16_t *dgu, *h;               // [S][2I], [S][I]: written by kGlu, read by the others
-    uint16_t *dx, *dw1, *dw2;        // NULL: not asked for
+    uint16_t *dgu, *h;               // [S][2I], [S][I]: written by kGradGlu (kFwdGlu: gu, h), read by the others
+    uint16_t *dx, *dw1, *dw2;        // NULL: not asked for; kFwdOut: dx is y
     int il;                          // gate/up row interleave
     float clamp;
 };
 
-// One tile of GradGlu or GradIn.
-template <Grad kKind, int TM>
-__device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsigned char *lds) {
-    using S = Shape<TM>;
-    // ---- operands P [S][K], Q [E][K][N], C [S][N]; tile: rows m0.. of expert e, columns n0..
-    const uint16_t *P = kKind == Grad::kGlu ? a.dy : a.dgu, *Q = kKind == Grad::kGlu ? a.w2 : a.w1;
-    uint16_t *C = kKind == Grad::kGlu ? a.h : a.dx;
-    const int K = kKind == Grad::kGlu ? a.H : 2 * a.I, N = kKind == Grad::kGlu ? a.I : a.H;
+// One tile of a product with the token rows on its rows.
+template <Gemm kKind, int TM>
+__device__ __forceinline__ void row_product(const GradArgs &a, int block, unsigned char *lds) {
+    constexpr bool kFwd = is_forward(kKind);
+    // the forward's waves take 64 columns, so that a lane has gate and up of the same hidden columns
+    using S = Shape<TM, kFwd ? TM / 64 : 4>;
+    // ---- operands P [S][K], Q [E][K][N] (forward: [E][N][K]), C [S][N]; tile: rows m0.. of expert e, columns n0..
+    const uint16_t *P = kKind == Gemm::kFwdGlu ? a.x : kKind == Gemm::kFwdOut ? a.h : kKind == Gemm::kGradGlu ? a.dy : a.dgu;
+    const uint16_t *Q = kKind == Gemm::kFwdGlu || kKind == Gemm::kGradIn ? a.w1 : a.w2;
+    uint16_t *C = kKind == Gemm::kGradGlu ? a.h : a.dx;
+    const int K = kKind == Gemm::kFwdOut ? a.I : kKind == Gemm::kGradIn ? 2 * a.I : a.H;
+    const int N = kKind == Gemm::kFwdGlu ? 2 * a.I : kKind == Gemm::kGradGlu ? a.I : a.H;
     int mt, nt;
     if (!row_tile(block, blocks_of(N, TM), a.n_tiles, mt, nt)) return;
     const int e = __builtin_amdgcn_readfirstlane(a.tiles[2 * mt]);
@@ -204,17 +221,25 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / kWaveN, wn = wave % kWaveN;
+    const int wm = wave / S::kWN, wn = wave % S::kWN;
     const int half = lane >> 5;
 
     // ---- DMAs of a stage: byte offsets of this lane's 16 bytes
     uint32_t offP[S::kOps], offQ[S::kOps];
 #pragma unroll
     for (int i = 0; i < S::kOps; ++i) {
-        const int r = wave * (kBK / kWaves) + i * S::kLines + lane / S::kChunks;  // stage row
-        const int c = tchunk(r, lane % S::kChunks) * 8;                           // column
-        // columns past N are not read (the last row's would lie behind the matrix)
-        offQ[i] = n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
+        if constexpr (kFwd) {
+            const int r = wave * (TM / kWaves) + i * 16 + (lane >> 2);  // weight row of the tile
+            int wr = n0 + r;
+            // GEMM1: tile rows are [gate 32 | up 32] of hidden columns n0 / 2 ..
+            if (kKind == Gemm::kFwdGlu && a.il == 0) wr = (r >> 5 & 1) * a.I + n0 / 2 + (r >> 6) * 32 + (r & 31);
+            offQ[i] = n0 + r < N ? (uint32_t)(wr * K + kchunk(r, lane & 3) * 8) * 2u : 0x80000000u;
+        } else {
+            const int r = wave * (kBK / kWaves) + i * S::kLines + lane / S::kChunks;  // stage row
+            const int c = tchunk(r, lane % S::kChunks) * 8;                           // column
+            // columns past N are not read (the last row's would lie behind the matrix)
+            offQ[i] = n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
+        }
         const int pr = wave * (TM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
         offP[i] = pr < live ? (uint32_t)(pr * K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
     }
@@ -231,7 +256,7 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
         }
         if (--left > 0) {
             sp += kBK * 2;
-            sq += kBK * 2 * N;
+            sq += kFwd ? kBK * 2 : kBK * 2 * N;
         }
     };
 
@@ -246,14 +271,16 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
     // NB: 32-row blocks of this wave with a live row
     auto mainloop = [&](auto nb_tag) {
         constexpr int NB = decltype(nb_tag)::value;
-        constexpr int NR = NB + 2 * S::kNX, NM = S::kNX * NB;  // LDS reads and MFMAs of a step
+        constexpr int NR = NB + (kFwd ? 1 : 2) * S::kNX, NM = S::kNX * NB;  // LDS reads and MFMAs of a step
         constexpr int G = 2 * S::kOps;                            // DMAs of a stage
         bf16x8 fq[2][S::kNX], fp[2][NB > 0 ? NB : 1];
         auto load = [&](int buf, int slot, int ks) {
             if constexpr (NB > 0) {
                 const unsigned char *s = lds + slot * S::kStage;
 #pragma unroll
-                for (int x = 0; x < S::kNX; ++x) fq[buf][x] = load_trans<TM>(s + S::kHalf, wn * S::kCols + x * 32, ks, lane);
+                for (int x = 0; x < S::kNX; ++x)
+                    fq[buf][x] = kFwd ? load_rows(s + S::kHalf, wn * S::kCols + x * 32, ks, lane)
+                                      : load_trans<TM>(s + S::kHalf, wn * S::kCols + x * 32, ks, lane);
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
                     fp[buf][b] = load_rows(s, wm * S::kRows + b * 32, ks, lane);
@@ -290,7 +317,7 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
     switch (nb_live) {
         case 4: if constexpr (S::kNB == 4) mainloop(std::integral_constant<int, 4>{}); break;
         case 3: if constexpr (S::kNB == 4) mainloop(std::integral_constant<int, 3>{}); break;
-        case 2: mainloop(std::integral_constant<int, 2>{}); break;
+        case 2: if constexpr (S::kNB >= 2) mainloop(std::integral_constant<int, 2>{}); break;
         case 1: mainloop(std::integral_constant<int, 1>{}); break;
         default: mainloop(std::integral_constant<int, 0>{}); break;
     }
@@ -298,7 +325,7 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
     // ---- epilogue: lane holds row wm kRows + b 32 + (lane & 31) and columns wn kCols + x 32 + 8 (v >>
     //      2) + 4 (lane >> 5) + (v & 3).  The tile goes through LDS, so that whole rows are read and stored.
     lds_barrier();
-    if constexpr (kKind == Grad::kGlu) {
+    if constexpr (kKind == Gemm::kGradGlu) {
         // dh goes through LDS in fp32, 128 columns at a time: a row of
         // 32 chunks of 4 values, chunk c of row r at c ^ (r & 31).  A thread then takes 8 columns of
         // eight rows: reads gate and up (three rows ahead), writes both gradients and h, each 16 bytes.  Buffer
@@ -364,26 +391,68 @@ __device__ __forceinline__ void grad_row_tile(const GradArgs &a, int block, unsi
         return;
     }
     auto cofs = [](int r, int c) { return r * (TM * 2) + ((c ^ (r & 15)) << 4); };
+    // a block's bf16 pair of 4 columns into chunk (wn kCols + x 32 + g4 8) / 8 of its row
+    auto stage_tile = [&]() {
 #pragma unroll
-    for (int b = 0; b < S::kNB; ++b) {
-        const int tr = wm * S::kRows + b * 32 + (lane & 31);
+        for (int b = 0; b < S::kNB; ++b) {
+            const int tr = wm * S::kRows + b * 32 + (lane & 31);
 #pragma unroll
-        for (int x = 0; x < S::kNX; ++x)
+            for (int x = 0; x < S::kNX; ++x)
+#pragma unroll
+                for (int g4 = 0; g4 < 4; ++g4) {
+                    u32x2 o;
+                    o.x = pack_bf16x2(acc[x][b][g4 * 4 + 0], acc[x][b][g4 * 4 + 1]);
+                    o.y = pack_bf16x2(acc[x][b][g4 * 4 + 2], acc[x][b][g4 * 4 + 3]);
+                    *(u32x2 *)(lds + cofs(tr, wn * (S::kCols / 8) + x * 4 + g4) + half * 8) = o;
+                }
+        }
+        lds_barrier();
+    };
+    const int ch = lane % S::kChunks, line = wave * S::kLines + lane / S::kChunks;  // this lane's chunk, first row
+    stage_tile();
+    if constexpr (kKind == Gemm::kFwdGlu) {
+        // gu first, in W1's stored row order: a contiguous run (interleaved rows), or TM / 2 gate and TM / 2 up
+        // columns I apart; then h = silu(g) u of the unrounded accumulators, TM / 2 columns
+        constexpr int kHC = S::kChunks / 2;
+        const int j = ch % kHC, part = ch / kHC;
+        const int tc = a.il == 0 ? (j >> 2) * 8 + part * 4 + (j & 3) : ch;
+        const int gc = a.il == 0 ? part * a.I + n0 / 2 + j * 8 : n0 + ch * 8;
+        if (n0 + ch * 8 < N) {
+#pragma unroll 4
+            for (int tr = line; tr < TM; tr += kWaves * S::kLines)
+                if (tr < live)
+                    *(u32x4 *)(a.dgu + (row0 + m0 + tr) * N + gc) = *(const u32x4 *)(lds + cofs(tr, tc));
+        }
+        lds_barrier();
+#pragma unroll
+        for (int b = 0; b < S::kNB; ++b) {
+            const int tr = wm * S::kRows + b * 32 + (lane & 31);
 #pragma unroll
             for (int g4 = 0; g4 < 4; ++g4) {
+                float hv[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) hv[q] = silu_mul(acc[0][b][g4 * 4 + q], acc[1][b][g4 * 4 + q], a.clamp);
                 u32x2 o;
-                o.x = pack_bf16x2(acc[x][b][g4 * 4 + 0], acc[x][b][g4 * 4 + 1]);
-                o.y = pack_bf16x2(acc[x][b][g4 * 4 + 2], acc[x][b][g4 * 4 + 3]);
-                *(u32x2 *)(lds + cofs(tr, wn * (S::kCols / 8) + x * 4 + g4) + half * 8) = o;
+                o.x = pack_bf16x2(hv[0], hv[1]);
+                o.y = pack_bf16x2(hv[2], hv[3]);
+                *(u32x2 *)(lds + cofs(tr, wn * 4 + g4) + half * 8) = o;
             }
-    }
-    lds_barrier();
-    const int ch = lane % S::kChunks, c = n0 + ch * 8;
-    if (c < N) {
-        uint16_t *out = C + (row0 + m0) * N + c;
+        }
+        lds_barrier();
+        const int hc = lane % kHC, hcol = n0 / 2 + hc * 8;
+        if (hcol < a.I) {
 #pragma unroll 4
-        for (int tr = wave * S::kLines + lane / S::kChunks; tr < TM; tr += kWaves * S::kLines)
-            if (tr < live) *(u32x4 *)(out + (int64_t)tr * N) = *(const u32x4 *)(lds + cofs(tr, ch));
+            for (int tr = (wave * 64 + lane) / kHC; tr < TM; tr += kThreads / kHC)
+                if (tr < live) *(u32x4 *)(a.h + (row0 + m0 + tr) * a.I + hcol) = *(const u32x4 *)(lds + cofs(tr, hc));
+        }
+    } else {
+        const int c = n0 + ch * 8;
+        if (c < N) {
+            uint16_t *out = C + (row0 + m0) * N + c;
+#pragma unroll 4
+            for (int tr = line; tr < TM; tr += kWaves * S::kLines)
+                if (tr < live) *(u32x4 *)(out + (int64_t)tr * N) = *(const u32x4 *)(lds + cofs(tr, ch));
+        }
     }
 }
 
@@ -437,7 +506,7 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
     const WeightTiles wt = weight_tiles<TM>(a.E, a.dw1 != nullptr, a.dw2 != nullptr, a.H, a.I);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / kWaveN, wn = wave % kWaveN;
+    const int wm = wave / S::kWN, wn = wave % S::kWN;
     const int half = lane >> 5;
     constexpr int G = 2 * S::kOps;  // DMAs of a stage
 
@@ -589,7 +658,19 @@ constexpr int waves_per_simd(int TM) { return TM == 256 ? 2 : 4; }
 template <int TM>
 __global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_glu_kernel(GradArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<TM>::kLds];
-    grad_row_tile<Grad::kGlu, TM>(a, blockIdx.x, lds);
+    row_product<Gemm::kGradGlu, TM>(a, blockIdx.x, lds);
+}
+
+// The forward for training of the layers that take small tiles (large ones run the forward's own kernels, whose 64-k
+// stages fetch whole cache lines of both operands: T = 4096, H = 2048, I = 1408, E = 64, k = 6 takes 530 us there and
+// 593 us with these products in 256 x 256 tiles).
+__global__ __launch_bounds__(kThreads, waves_per_simd(128)) void forward_glu_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<128>::kLds];
+    row_product<Gemm::kFwdGlu, 128>(a, blockIdx.x, lds);
+}
+__global__ __launch_bounds__(kThreads, waves_per_simd(128)) void forward_out_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<128>::kLds];
+    row_product<Gemm::kFwdOut, 128>(a, blockIdx.x, lds);
 }
 
 // GradIn (the first in_blocks workgroups) and GradWeight, which all need GradGlu's results only: in one launch
@@ -599,7 +680,7 @@ template <int TM>
 __global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_products_kernel(GradArgs a, int in_blocks) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<TM>::kLds];
     if ((int)blockIdx.x < in_blocks)
-        grad_row_tile<Grad::kIn, TM>(a, blockIdx.x, lds);
+        row_product<Gemm::kGradIn, TM>(a, blockIdx.x, lds);
     else
         grad_weight_tiles<TM>(a, blockIdx.x - in_blocks, lds);
 }
@@ -631,10 +712,31 @@ hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const
                                     uint16_t *dw2, hipStream_t s) {
     const GradArgs a = {offsets, tiles, n_tiles, (const int4 *)order, p.E, p.H, p.I, dy, x, (const uint16_t *)w.w1,
                         (const uint16_t *)w.w2, gu, dgu, h, dx, dw1, dw2, p.glu_interleave, p.swiglu_clamp};
-    // 256 x 256 tiles unless their number leaves CUs idle
-    if (grad_max_tiles(p, 256) * blocks_of(p.H, 256) > kSmallTiles)
-        return launch<256>(a, p, tiles, n_tiles, (int4 *)order, s);
-    return launch<128>(a, p, tiles, n_tiles, (int4 *)order, s);
+    return small_tiles(p) ? launch<128>(a, p, tiles, n_tiles, (int4 *)order, s)
+                          : launch<256>(a, p, tiles, n_tiles, (int4 *)order, s);
+}
+
+bool ffn_train_small(const moe_problem &p, size_t list_bytes) {
+    return small_tiles(p) && 16 + 8 * (size_t)grad_max_tiles(p, 128) <= list_bytes;
+}
+
+hipError_t launch_ffn_train_small_bf16(const uint16_t *x, const int32_t *offsets, const moe_weights &w,
+                                       const moe_problem &p, int32_t *list, uint16_t *gu, uint16_t *h, uint16_t *y,
+                                       hipStream_t s) {
+    constexpr int TM = 128;
+    GradArgs a = {};
+    int32_t *n_tiles = list, *tiles = list + 4;
+    a.offsets = offsets, a.tiles = tiles, a.n_tiles = n_tiles, a.E = p.E, a.H = p.H, a.I = p.I;
+    a.x = x, a.w1 = (const uint16_t *)w.w1, a.w2 = (const uint16_t *)w.w2, a.dgu = gu, a.h = h, a.dx = y;
+    a.il = p.glu_interleave, a.clamp = p.swiglu_clamp;
+    const int64_t max_tiles = grad_max_tiles(p, TM);
+    hipLaunchKernelGGL(grad_prepare_kernel, dim3(1), dim3(256), 0, s, offsets, p.E, TM, tiles, n_tiles, (int4 *)nullptr);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(forward_glu_kernel, dim3(row_blocks(max_tiles, blocks_of(2 * p.I, TM))), dim3(kThreads), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(forward_out_kernel, dim3(row_blocks(max_tiles, blocks_of(p.H, TM))), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace tpg

@@ -565,7 +565,14 @@ int moe_grouped_ffn_train(const void *x_perm, const int32_t *offsets, const moe_
     if (!x_perm || !offsets || !gu || !y_perm || !ws) return MOE_ERR_NULL;
     if ((st = check_weights(w, p)) || (st = check_aligned(x_perm, w->w1, w->w2, gu, y_perm, ws))) return st;
     if (ws_bytes < moe_call_workspace_bytes(p, MOE_WS_GROUPED_FFN)) return MOE_ERR_WORKSPACE;
-    return run_grouped_ffn(x_perm, nullptr, offsets, *w, *p, y_perm, (char *)ws, stream, gu);
+    const WsLayout L = ws_layout(*p);
+    char *b = (char *)ws;
+    // small tiles' list takes the place of the forward's list and count, which lie before h
+    if (ffn_train_small(*p, L.h - L.tiles))
+        return hip_status(launch_ffn_train_small_bf16((const uint16_t *)x_perm, offsets, *w, *p,
+                                                      (int32_t *)(b + L.tiles), (uint16_t *)gu, (uint16_t *)(b + L.h),
+                                                      (uint16_t *)y_perm, stream));
+    return run_grouped_ffn(x_perm, nullptr, offsets, *w, *p, y_perm, b, stream, gu);
 }
 
 int moe_grouped_ffn_backward(const void *dy_perm, const void *x_perm, const void *gu, const int32_t *offsets,

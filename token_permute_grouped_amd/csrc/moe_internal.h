@@ -142,6 +142,13 @@ hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const
                                     int32_t *order, uint16_t *dgu, uint16_t *h, uint16_t *dx, uint16_t *dw1,
                                     uint16_t *dw2, hipStream_t s);
 
+// The grouped FFN keeping gu [S][2I], the pre-activations in W1's stored row order, in small tiles, for the layers that
+// ffn_train_small names; h [S][I] and list (16 + 8 grad_max_tiles(p, 128) bytes) are scratch
+bool ffn_train_small(const moe_problem &p, size_t list_bytes);
+hipError_t launch_ffn_train_small_bf16(const uint16_t *x, const int32_t *offsets, const moe_weights &w,
+                                       const moe_problem &p, int32_t *list, uint16_t *gu, uint16_t *h, uint16_t *y,
+                                       hipStream_t s);
+
 // row_src NULL: x_perm / x_perm_scale are the expert-ordered rows; else x / x_scale token rows
 // read through row_src (the gather fused into GEMM1; needs gather_fits_fp8(T, H)).  row_dst as
 // for launch_gemm2_bf16.
