@@ -115,7 +115,14 @@ __device__ __forceinline__ bf16x8 load_trans(const unsigned char *stage, int n0,
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// k along the rows: the logical chunk that chunk position p of row r holds, and the fragment of rows r0..
+// k along the rows, 64 k a row (128 bytes, a cache line): chunk c of row r at c ^ (r & 7) ^ (r >> 3 & 1)
+__device__ __forceinline__ int lchunk(int r, int p) { return p ^ (r & 7) ^ (r >> 3 & 1); }
+__device__ __forceinline__ bf16x8 load_lines(const unsigned char *stage, int r0, int ks, int lane) {
+    const int r = r0 + (lane & 31);
+    return *(const bf16x8 *)(stage + r * 128 + (lchunk(r, ks * 2 + (lane >> 5)) << 4));
+}
+
+// k along the rows, 32 k a row: the logical chunk that chunk position p of row r holds, and the fragment of rows r0..
 __device__ __forceinline__ int kchunk(int r, int p) { return p ^ ((r >> 2) & 3); }
 __device__ __forceinline__ bf16x8 load_rows(const unsigned char *stage, int r0, int ks, int lane) {
     const int r = r0 + (lane & 31);
@@ -225,7 +232,9 @@ __device__ __forceinline__ void row_product(const GradArgs &a, int block, unsign
     const int half = lane >> 5;
 
     // ---- DMAs of a stage: byte offsets of this lane's 16 bytes
-    uint32_t offP[S::kOps], offQ[S::kOps];
+    // (gradients: P's stages are 64 k, whole cache lines of its rows)
+    constexpr int kOpsP = kFwd ? S::kOps : 2 * S::kOps;
+    uint32_t offP[kOpsP], offQ[S::kOps];
 #pragma unroll
     for (int i = 0; i < S::kOps; ++i) {
         if constexpr (kFwd) {
@@ -240,24 +249,32 @@ __device__ __forceinline__ void row_product(const GradArgs &a, int block, unsign
             // columns past N are not read (the last row's would lie behind the matrix)
             offQ[i] = n0 + c >= N ? 0x80000000u : (uint32_t)(r * N + n0 + c) * 2u;
         }
-        const int pr = wave * (TM / kWaves) + i * 16 + (lane >> 2);  // tile row, four chunks each
-        offP[i] = pr < live ? (uint32_t)(pr * K + kchunk(pr, lane & 3) * 8) * 2u : 0x80000000u;
     }
-    const uint32_t lds0 = lds_address(lds) + wave * (S::kOps * 1024);
-    i32x4 rp = buffer(P + (row0 + m0) * K, live * K * 2), rq = buffer(Q + (int64_t)e * K * N, K * N * 2);
-    int sp = 0, sq = 0, left = nk;  // the next stage's offsets in P's rows and in Q, and stages left
-    auto request = [&](int slot) {
-        const uint32_t dst = lds0 + slot * S::kStage;
-        if (left == 0) rp.z = rq.z = 0;  // behind the last stage: out of bounds, nothing is read
 #pragma unroll
-        for (int i = 0; i < S::kOps; ++i) {
-            dma(rp, offP[i], sp, dst + i * 1024);
-            dma(rq, offQ[i], sq, dst + S::kHalf + i * 1024);
-        }
-        if (--left > 0) {
-            sp += kBK * 2;
-            sq += kFwd ? kBK * 2 : kBK * 2 * N;
-        }
+    for (int i = 0; i < kOpsP; ++i) {
+        const int pr = wave * (TM / kWaves) + (kFwd ? i * 16 + (lane >> 2) : i * 8 + (lane >> 3));  // tile row
+        const int c = kFwd ? kchunk(pr, lane & 3) : lchunk(pr, lane & 7);
+        offP[i] = pr < live ? (uint32_t)(pr * K + c * 8) * 2u : 0x80000000u;
+    }
+    const uint32_t lds0 = lds_address(lds);
+    // the next stage's offsets in P's rows and in Q; behind the last one nothing is in bounds
+    const uint16_t *p0 = P + (row0 + m0) * K, *q0 = Q + (int64_t)e * K * N;
+    int sp = 0, sq = 0, np = live * K * 2, nq = K * N * 2;
+    auto request_p = [&](uint32_t dst) {
+        dst += wave * (kOpsP * 1024);
+        const i32x4 rp = buffer(p0, np);
+#pragma unroll
+        for (int i = 0; i < kOpsP; ++i) dma(rp, offP[i], sp, dst + i * 1024);
+        sp += kFwd ? kBK * 2 : kBK * 4;
+        if (sp == K * 2) np = 0;
+    };
+    auto request_q = [&](uint32_t dst) {
+        dst += wave * (S::kOps * 1024);
+        const i32x4 rq = buffer(q0, nq);
+#pragma unroll
+        for (int i = 0; i < S::kOps; ++i) dma(rq, offQ[i], sq, dst + i * 1024);
+        sq += kFwd ? kBK * 2 : kBK * 2 * N;
+        if (sq == (kFwd ? K * 2 : K * N * 2)) nq = 0;
     };
 
     f32x16 acc[S::kNX][S::kNB];
@@ -272,18 +289,18 @@ __device__ __forceinline__ void row_product(const GradArgs &a, int block, unsign
     auto mainloop = [&](auto nb_tag) {
         constexpr int NB = decltype(nb_tag)::value;
         constexpr int NR = NB + (kFwd ? 1 : 2) * S::kNX, NM = S::kNX * NB;  // LDS reads and MFMAs of a step
-        constexpr int G = 2 * S::kOps;                            // DMAs of a stage
         bf16x8 fq[2][S::kNX], fp[2][NB > 0 ? NB : 1];
-        auto load = [&](int buf, int slot, int ks) {
+        // fragments of step `ps` of P's stage at p and step `qs` of Q's at q
+        auto load = [&](int buf, const unsigned char *p, int ps, const unsigned char *q, int qs) {
             if constexpr (NB > 0) {
-                const unsigned char *s = lds + slot * S::kStage;
 #pragma unroll
                 for (int x = 0; x < S::kNX; ++x)
-                    fq[buf][x] = kFwd ? load_rows(s + S::kHalf, wn * S::kCols + x * 32, ks, lane)
-                                      : load_trans<TM>(s + S::kHalf, wn * S::kCols + x * 32, ks, lane);
+                    fq[buf][x] = kFwd ? load_rows(q, wn * S::kCols + x * 32, qs, lane)
+                                      : load_trans<TM>(q, wn * S::kCols + x * 32, qs, lane);
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    fp[buf][b] = load_rows(s, wm * S::kRows + b * 32, ks, lane);
+                    fp[buf][b] = kFwd ? load_rows(p, wm * S::kRows + b * 32, ps, lane)
+                                      : load_lines(p, wm * S::kRows + b * 32, ps, lane);
             }
         };
         auto mfmas = [&](int buf) {
@@ -293,23 +310,73 @@ __device__ __forceinline__ void row_product(const GradArgs &a, int block, unsign
                 for (int x = 0; x < S::kNX; ++x)
                     acc[x][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[buf][x], fp[buf][b], acc[x][b], 0, 0, 0);
         };
+        if constexpr (kFwd) {
+            constexpr int G = 2 * S::kOps;  // DMAs of a stage
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) request(s);
-        wait_vmcnt<(kStages - 1) * G>();
-        lds_barrier();
-        load(0, 0, 0);
-        int slot = 0;
-        for (int kt = 0; kt < nk; ++kt) {
-            load(1, slot, 1);
-            mfmas(0);
-            if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
-            wait_vmcnt<(kStages - 2) * G>();  // stage kt+1 has landed; kt+2 .. kt+4 may be in flight
+            for (int s = 0; s < kStages; ++s) {
+                request_p(lds0 + s * S::kStage);
+                request_q(lds0 + s * S::kStage + S::kHalf);
+            }
+            wait_vmcnt<(kStages - 1) * G>();
             lds_barrier();
-            request(slot);
-            slot = slot + 1 == kStages ? 0 : slot + 1;
-            load(0, slot, 0);
-            mfmas(1);
-            if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+            load(0, lds, 0, lds + S::kHalf, 0);
+            int slot = 0;
+            for (int kt = 0; kt < nk; ++kt) {
+                const unsigned char *st = lds + slot * S::kStage;
+                load(1, st, 1, st + S::kHalf, 1);
+                mfmas(0);
+                if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+                wait_vmcnt<(kStages - 2) * G>();  // stage kt+1 has landed; kt+2 .. kt+4 may be in flight
+                lds_barrier();
+                request_p(lds0 + slot * S::kStage);
+                request_q(lds0 + slot * S::kStage + S::kHalf);
+                slot = slot + 1 == kStages ? 0 : slot + 1;
+                load(0, lds + slot * S::kStage, 0, lds + slot * S::kStage + S::kHalf, 0);
+                mfmas(1);
+                if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+            }
+        } else {
+            // P: three 64-k stages; Q: four 32-k stages behind them.  Requests go P0 Q0 Q1 P1 Q2 Q3 P2, then Q s+4 when
+            // every wave has read Q s, and P j+3 when it has read P j (after Q 2j+5).  Before Q s+1 is read, for odd s
+            // with P (s+1)/2, what was requested after them may be in flight: even s P j+1, Q s+2, Q s+3, P j+2; odd s
+            // Q s+2, P j+2, Q s+3.
+            constexpr int kP = 2 * S::kHalf, kQ = 3 * kP, OP = kOpsP, OQ = S::kOps;
+            request_p(lds0);
+            request_q(lds0 + kQ);
+            request_q(lds0 + kQ + S::kHalf);
+            request_p(lds0 + kP);
+            request_q(lds0 + kQ + 2 * S::kHalf);
+            request_q(lds0 + kQ + 3 * S::kHalf);
+            request_p(lds0 + 2 * kP);
+            wait_vmcnt<2 * OP + 3 * OQ>();  // P0 and Q0 have landed
+            lds_barrier();
+            load(0, lds, 0, lds + kQ, 0);
+            int pslot = 0, qslot = 0;  // of stage j; 0 or 2: of stage s = 2 j
+            for (int j = 0; j < nk / 2; ++j) {
+                const unsigned char *p = lds + pslot * kP, *q = lds + kQ + qslot * S::kHalf;
+                load(1, p, 1, q, 1);
+                mfmas(0);
+                if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+                wait_vmcnt<2 * OP + 2 * OQ>();
+                lds_barrier();
+                request_q(lds0 + kQ + qslot * S::kHalf);
+                q += S::kHalf;
+                load(0, p, 2, q, 0);
+                mfmas(1);
+                if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+                load(1, p, 3, q, 1);
+                mfmas(0);
+                if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+                wait_vmcnt<OP + 2 * OQ>();
+                lds_barrier();
+                request_q(lds0 + kQ + (qslot + 1) * S::kHalf);
+                request_p(lds0 + pslot * kP);
+                pslot = pslot == 2 ? 0 : pslot + 1;
+                qslot ^= 2;
+                load(0, lds + pslot * kP, 0, lds + kQ + qslot * S::kHalf, 0);
+                mfmas(1);
+                if constexpr (NB > 0) interleave_ds_mfma<NR, NM>();
+            }
         }
         wait_vmcnt<0>();  // the LDS is written again below
     };
