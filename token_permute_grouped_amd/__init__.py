@@ -281,8 +281,7 @@ def _bad_tensor(fn, t, n):
 
 
 def _pointers(fn: str, T: int, sizes):
-    """(device index, addresses) of sizes = ((tensor, address or None; bytes), ...); the index is None
-    without tensors"""
+    """(device index, addresses) of sizes = ((tensor, address or None; bytes), ...); the index is None without tensors"""
     dev, ptrs = None, []
     for t, n in sizes:
         if t is None or t.__class__ is int:
@@ -290,11 +289,10 @@ def _pointers(fn: str, T: int, sizes):
             continue
         if not t.is_contiguous() or t.nbytes < n:
             _bad_tensor(fn, t, n)
-        d = t.get_device()
-        if d != dev:
-            if dev is not None:
-                raise ValueError(f"{fn}: tensors on different devices")
-            dev = d
+        if dev is None:
+            dev = t.get_device()
+        elif dev != t.get_device():
+            raise ValueError(f"{fn}: tensors on different devices")
         ptrs.append(t.data_ptr())
     if dev == -1 and T > 0:
         raise ValueError(f"{fn}: tensors that are not on a GPU")
@@ -303,11 +301,16 @@ def _pointers(fn: str, T: int, sizes):
 
 def _call(fn: str, dev, stream, *args):
     f = getattr(_lib, fn)
-    if dev is None or dev < 0 or dev == _torch.cuda.current_device():
+    if dev is None or dev < 0:
         st = f(*args, _stream(stream))
     else:
-        with _torch.cuda.device(dev):
-            st = f(*args, _stream(stream))
+        # the device's current stream, without a stream object
+        s = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        if dev == _torch._C._cuda_getDevice():
+            st = f(*args, s)
+        else:
+            with _torch.cuda.device(dev):
+                st = f(*args, s)
     if st != MOE_OK:
         _check(fn, st)
 

@@ -28,13 +28,12 @@ __global__ __launch_bounds__(256) void route_topk_kernel(const float *__restrict
 // route_row's rounds (ids, exp and d in each).
 // V: experts per lane (16 V >= E).  kWide: k > 16, d is loaded after the rounds.
 template <int V, bool kIds>
-__device__ __forceinline__ void choose(const float *__restrict__ l, int E, int k, int i, int (&slot)[V], float &lmax) {
+__device__ __forceinline__ void choose(const float (&l)[V], int E, int k, int i, int (&slot)[V], float &lmax) {
     using namespace route_detail;
     uint32_t key[V];
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-        const int e = i + 16 * q;
-        key[q] = e < E ? logit_key(l[e]) : 0u;
+        key[q] = i + 16 * q < E ? logit_key(l[q]) : 0u;
         slot[q] = -1;
     }
     for (int j = 0; j < k; ++j) {
@@ -74,7 +73,9 @@ __device__ __forceinline__ void route_row_backward(const float *__restrict__ log
                                                    const float *__restrict__ dtopk_w, int64_t t, bool valid, int E,
                                                    int k, int lane, float *__restrict__ dlogits) {
     const int i = lane & 15;
-    const float *l = logits + t * E;
+    float l[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) l[q] = logits[t * E + min(i + 16 * q, E - 1)];
     auto slot_grad = [&](int j) {
         const int64_t s = t * k + j;
         return slot_drop != nullptr && slot_drop[s] != 0 ? 0.0f : dtopk_w[s];
@@ -90,8 +91,7 @@ __device__ __forceinline__ void route_row_backward(const float *__restrict__ log
     float ex[V], d[V], z = 0.0f, zd = 0.0f;
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-        const int e = i + 16 * q;
-        ex[q] = slot[q] >= 0 ? expf(l[min(e, E - 1)] - lmax) : 0.0f;
+        ex[q] = slot[q] >= 0 ? expf(l[q] - lmax) : 0.0f;
         if constexpr (kWide)
             d[q] = slot[q] >= 0 ? slot_grad(slot[q]) : 0.0f;
         else
