@@ -7,7 +7,7 @@ import torch
 
 import token_permute_grouped_amd as tpg
 from moe_synth import MoeConfig, generate
-from tests._block import FP32, HALF, bf16, close, combine, dev, nan, rms, routing, workspace
+from tests._block import FP32, HALF, bf16, close, combine, dev, nan, rms, routing, tables, workspace
 from tests._gpu import DEV, DeviceProblem
 
 pytestmark = pytest.mark.gpu
@@ -224,6 +224,31 @@ def test_combine_norm_backward(T, H, E, k, drop, form, gate, residual):
     again = y.clone()
     tpg.moe_combine_norm_backward(dev(dout), again, slot_row, tw, c["norm"], c["residual"], p, again)
     assert torch.equal(again[:R], dy[:R])
+
+
+@pytest.mark.parametrize("T,H,k", [(5, 640, 1), (40, 4096, 1), (33, 256, 3), (2, 16512, 1), (7, 384, 9)])
+def test_weight_gradient_of_a_token_with_one_live_slot(T, H, k):
+    """the norm takes a single weight out again but for eps: dtopk_w = r^3 eps (b . y), a difference of two numbers
+    that agree to five digits and more if it is not computed as that"""
+    g = _gen(T, H, k)
+    idx = torch.full((T, k), -1)
+    idx[torch.arange(T), torch.randint(0, k, (T,), generator=g)] = torch.randint(0, 4, (T,), generator=g)
+    offsets, slot_row = tables(idx, 4)
+    y, dout, w = bf16(T * k, H, g=g), bf16(T, H, g=g), bf16(H, g=g)
+    tw = torch.rand(T, k, generator=g) + 0.1
+    p = tpg.make_problem(T, H, 256, max(4, k), k)
+    dtw = nan(T, k, dtype=torch.float32)
+    keep = dev(w)
+    tpg.moe_combine_norm_backward(dev(dout), dev(y), dev(slot_row), dev(tw), tpg.make_norm(keep, EPS), None, p,
+                                  nan(T * k, H), dtw)
+    live = slot_row >= 0
+    rows = y.double()[slot_row[live].long()]
+    c = rows * tw[live].double()[:, None]
+    r = torch.rsqrt((c * c).mean(1) + EPS)
+    by = dout.double() * w.double() * rows
+    want, size = torch.zeros(T, k, dtype=torch.float64), torch.zeros(T, k, dtype=torch.float64)
+    want[live], size[live] = r ** 3 * EPS * by.sum(1), r ** 3 * EPS * by.abs().sum(1)
+    close(dtw, want, FP32 * size, "dtopk_w", half=0.0)
 
 
 @pytest.mark.parametrize("prec,flags", [("bf16", 0), ("bf16", tpg.MOE_FLAG_SCATTER_Y), ("w4a8", 0),

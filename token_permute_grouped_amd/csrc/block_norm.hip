@@ -418,6 +418,10 @@ __global__ __launch_bounds__(1024) void combine_norm_kernel(const uint4 *__restr
     }
 }
 
+// A token with one live slot: c = w y, and its weight's gradient r b . y - r^3 mean(b c) (c . y) is r (b . y) (1 - r^2
+// mean(c^2)) = r^3 eps (b . y): the norm takes the weight out again but for eps.  It is computed in that form; the
+// difference would leave rounding errors a hundred thousand times its size.
+//
 // Per channel both the norm's weight and a channel gate are one factor f = gate weight (1 where there is none), so that
 // b = token_gate f dout.  One sum over tokens then serves both gradients: with a = sum_t token_gate dout c r,
 // dweight = gate a and dgate = weight a (formed by column_sum), and a token gate's gradient is r (f dout . c).
@@ -474,6 +478,10 @@ __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(
             }
             if (dresidual) dresidual[t * row_vec + c] = combine_pack8(o);
         }
+        int n_live = 0;
+        for (int j = 0; j < k; ++j) n_live += slots[j] >= 0;
+        const bool one = n.on && n_live == 1;
+        const float one_c = one ? coef : 0.f, one_r = one ? r * n.eps * r : 1.0f;  // r b = dc + coef c
         for (int j0 = 0; j0 < k; j0 += 8, flip ^= 1) {
             float dot[8] = {};
 #pragma unroll
@@ -494,7 +502,7 @@ __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(
                     unpack8(v[q], f);
 #pragma unroll
                     for (int z = 0; z < 8; ++z) {
-                        dot[q] = fmaf(d_[i][z], f[z], dot[q]);
+                        dot[q] = fmaf(fmaf(one_c, c_[i][z], d_[i][z]), f[z], dot[q]);
                         o[z] = tw[j0 + q] * d_[i][z];
                     }
                     dy[(int64_t)slots[j0 + q] * row_vec + c] = combine_pack8(o);
@@ -511,7 +519,7 @@ __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(
                 if (threadIdx.x < 8 && j < k) {
                     float sum = 0.f;
                     for (int w = 0; w < nw; ++w) sum += dots[flip][w * 8 + threadIdx.x];
-                    dtopk_w[t * k + j] = slots[j] >= 0 ? sum : 0.f;
+                    dtopk_w[t * k + j] = slots[j] >= 0 ? sum * one_r : 0.f;
                 }
             }
         }
@@ -609,7 +617,11 @@ __global__ __launch_bounds__(1024) void combine_norm_backward8_kernel(
                 sd += red[flip][v][threadIdx.x];
                 sc += red[flip][v][8 + threadIdx.x];
             }
-            dtopk_w[t * k + threadIdx.x] = slot_row[t * k + threadIdx.x] >= 0 ? r * tok * sd - coef * sc : 0.f;
+            int n_live = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) n_live += cur.row[q] >= 0;
+            const float g = n.on && n_live == 1 ? r * n.eps * r * r * tok * sd : r * tok * sd - coef * sc;
+            dtopk_w[t * k + threadIdx.x] = slot_row[t * k + threadIdx.x] >= 0 ? g : 0.f;
         }
         if (dgate_token && threadIdx.x == 0) dgate_token[t] = sums[1] * r;
         if (!in) continue;
