@@ -322,7 +322,7 @@ int moe_w4a8_tile_weights(const void *codes, const void *bscale, void *codes_til
  * the expert outputs are bf16 rows in all of them.  Reductions and intermediate values are
  * fp32; each output is rounded once, to nearest even.  No atomics: results are reproducible
  * bit for bit.  With T == 0 the sums over tokens (dweight, a channel gate's dgate, dw1, dw2) are set
- * to 0 and nothing else happens.  Beyond the checks above, arrays of rows must be 16-byte aligned
+ * to 0 and nothing else happens.  Rows, weights, channel gates and their gradients must be 16-byte aligned
  * (MOE_ERR_UNSUPPORTED otherwise).  An output may not overlap an input unless said so. */
 
 /* RMS norm of a row v of H values: v * rsqrt(mean(v^2) + eps) * weight.  Where a call takes a

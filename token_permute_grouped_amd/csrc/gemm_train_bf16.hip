@@ -1,40 +1,49 @@
-// The four products of the grouped FFN's backward pass in bf16 on CDNA4 matrix cores
-// (v_mfma_f32_32x32x16_bf16), for the rows r of every expert e:
+// The products of the grouped FFN's training step in bf16 on CDNA4 matrix cores (v_mfma_f32_32x32x16_bf16), for the
+// rows r of every expert e:
 //
-//     dh  = dy W2_e        then dgu and h from dh and the kept gu      (GradGlu)    2 R H I flops
-//     dx  = dgu W1_e                                                  (GradIn)     4 R H I
-//     dW1_e = dgu^T x      dW2_e = dy^T h     (sums over e's rows)    (GradWeight) 4 and 2 R H I
+//     dh  = dy W2_e        then dgu and h from dh and the kept gu      (kGradGlu)    2 R H I flops
+//     dx  = dgu W1_e                                                  (kGradIn)     4 R H I
+//     dW1_e = dgu^T x      dW2_e = dy^T h     (sums over e's rows)    (weights)    4 and 2 R H I
+//     gu = x W1_e^T, h = silu(gate) up;  y = h W2_e^T                 (kFwdGlu, kFwdOut: small layers only)
 //
-// All of them are C[i][j] = sum_k P[i or k] Q[k][j]: Q has the sum's index on its rows (weights as they are
-// stored, or token rows), P has it along its rows (GradGlu, GradIn: token rows) or on them (GradWeight).  The
-// operands with k on their rows would need a transposed copy for plain fragment reads (17 GB of traffic
-// on the layer with T = 16384, H = 4096, I = 2048, E = 128, k = 8); here they go into LDS as they are and come out
-// through its transposing reads (load_trans).
+// Backward, all of them are C[i][j] = sum_k P[i or k] Q[k][j]: Q has the sum's index on its rows (weights as they are
+// stored, or token rows), P has it along its rows (kGradGlu, kGradIn: token rows) or on them (weights).  The operands
+// with k on their rows would need a transposed copy for plain fragment reads (17 GB of traffic on the layer with T =
+// 16384, H = 4096, I = 2048, E = 128, k = 8, called the large layer below); here they go into LDS as they are and come
+// out through its transposing reads (load_trans).
 //
-// Tile and pipeline.  A workgroup of 8 waves owns a 256 x 256 output tile, 128 x 64 per wave (4 x 2 blocks of 32 x
-// 32), two waves per SIMD.  A stage is 32 k of both operands, 32 KB, in a ring of five: every operand goes
-// straight to LDS by 16-byte-per-lane DMAs, requested five stages ahead.  A stage's one barrier stands
-// before its second 16-k step: by then every wave has read the stage's fragments, so its slot takes the DMAs
-// of the stage five ahead, and the next stage's first fragments load under the step's MFMAs.  The DMAs of
-// stages past the end are issued too (out of bounds, so nothing is read), so that one wait count fits every stage.
+// Tile and pipeline.  A workgroup of 8 waves owns a 256 x 256 tile, 128 x 64 per wave (4 x 2 blocks of 32 x 32), two
+// waves per SIMD.  Every operand goes straight to LDS by 16-byte-per-lane DMAs, two 64-k stages ahead or more: in the
+// weight gradients a ring of five 32-k stages of both operands (32 KB each); in kGradGlu and kGradIn three 64-k stages
+// of P, whose rows are then whole cache lines, and four 32-k stages of Q.  Per 32 k there is one barrier, which stands
+// before the second 16-k step: by then every wave has read the stage's fragments, so its place takes new requests, and
+// the next stage's first fragments load under the step's MFMAs.  Requests behind the last stage are made too, out of
+// bounds, so that one wait count fits every stage.
 //
-// The DMAs are inline assembly: the compiler waits for every DMA it knows of (vmcnt(0)) before a
-// transposing LDS read, which drained the ring each stage (dW1 of the layer above 6.4 ms, GradIn 4.5 ms).
+// The DMAs are inline assembly: the compiler waits for every DMA it knows of (vmcnt(0)) before a transposing LDS read,
+// which drained the ring each stage (dW1 of the large layer 6.4 ms, kGradIn 4.5 ms; without the drains 4.6 and 4.2).
 // They have no register outputs; wait_vmcnt and the barriers order them.
 //
-// LDS layout of a stage.  k on the rows: a row is 256 columns of one k, 512 bytes, sixteen 32-byte segments,
-// segment s of row r at s ^ 2 (r & 3); the transposing reads of 32 lanes then touch 8 distinct segments, one
-// per bank group.  k along the rows: a row is 32 k, 64 bytes, four 16-byte chunks, chunk c of row r at c ^ ((r >>
-// 2) & 3), so that 16 rows' reads touch all 16 bank groups.  The DMA's lanes fetch the chunk their place holds.
+// Layers whose 256 x 256 tiles would leave CUs idle take 128 x 128 tiles in half the LDS, two workgroups per CU
+// (small_tiles).
 //
-// Ragged ends.  Rows past the tile's or the expert's last read as zero by the buffers' bounds (GradWeight
-// sets base and bound for every stage, which also keeps row offsets 64-bit).  Columns past the matrix's
-// width are computed from whatever follows in memory within the bounds and are not stored.  GradGlu and GradIn
-// skip the MFMAs of 32-row blocks without a live row.
+// What bounds it.  The large layer's backward pass takes 13.5 ms, 0.98 PFLOP/s: the matrix cores are busy 63 % of the
+// cycles in the second launch (56 % in kGradGlu) at the 1.5 GHz that the board's power limit leaves (a library bf16
+// product of 16384^3 runs 1.35 PFLOP/s there with this operand order).  Experts of few rows are bound by the stores of
+// their weight gradients (128 experts of 32 rows, 6.4 GB of gradients: 2.0 ms with dx).
 //
-// Work order.  GradGlu and GradIn take m-tiles from the tile list by tile_map, as the forward does.
-// GradWeight takes the experts largest first; runs of 32 neighbouring tiles (4 x 8) go to one XCD (block index mod
-// 8), which works on them at once and shares their row and column slabs in its L2.
+// LDS layout of a stage.  k on the rows: a row is TM columns of one k, 32-byte segments, segment s of row r at s ^ 2 (r
+// & 3); the transposing reads of 32 lanes then touch 8 distinct segments, one per bank group.  k along the rows, 32 k
+// (64 bytes) or 64 k (128 bytes): 16-byte chunks, permuted by the row so that 16 rows' reads touch all 16 bank groups
+// (kchunk, lchunk).  The DMA's lanes fetch the chunk that their place holds.
+//
+// Ragged ends.  Rows past the tile's or the expert's last read as zero by the buffers' bounds (the weight gradients set
+// base and bound for every stage, which also keeps row offsets 64-bit).  Columns past the matrix's width are computed
+// from whatever follows in memory within the bounds and are not stored.  The row products skip the MFMAs of 32-row
+// blocks without a live row.
+//
+// Work order.  The row products take m-tiles from the tile list by tile_map, as the forward does.  The weight gradients
+// take the experts largest first (weight_tiles).
 #include <type_traits>
 
 #include "gemm_common.h"
@@ -193,7 +202,7 @@ __global__ __launch_bounds__(256) void grad_prepare_kernel(const int32_t *__rest
     order[rank] = make_int4(e, offsets[e], cnt[e], 0);
 }
 
-struct GradArgs {
+struct TrainArgs {
     const int32_t *offsets;          // [E+1]
     const int32_t *tiles, *n_tiles;  // m-tiles of the products with token rows
     const int4 *order;               // {expert, first row, rows}, most rows first
@@ -207,7 +216,7 @@ struct GradArgs {
 
 // One tile of a product with the token rows on its rows.
 template <Gemm kKind, int TM>
-__device__ __forceinline__ void row_product(const GradArgs &a, int block, unsigned char *lds) {
+__device__ __forceinline__ void row_product(const TrainArgs &a, int block, unsigned char *lds) {
     constexpr bool kFwd = is_forward(kKind);
     // the forward's waves take 64 columns, so that a lane has gate and up of the same hidden columns
     using S = Shape<TM, kFwd ? TM / 64 : 4>;
@@ -533,7 +542,7 @@ struct WeightTile {
     bool live;
 };
 template <int TM>
-__device__ __forceinline__ WeightTile weight_tile(const GradArgs &a, const WeightTiles &wt, int g) {
+__device__ __forceinline__ WeightTile weight_tile(const TrainArgs &a, const WeightTiles &wt, int g) {
     WeightTile w = {};
     w.live = g < wt.total;
     if (!w.live) return w;
@@ -568,7 +577,7 @@ __device__ __forceinline__ WeightTile weight_tile(const GradArgs &a, const Weigh
 // Waiting for fewer than n outstanding requests is right whatever the stores do: they only make the count larger.
 // (One tile per workgroup, with the whole ring filled and drained for each: 8 us more per tile.)
 template <int TM>
-__device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, unsigned char *lds) {
+__device__ __forceinline__ void grad_weight_tiles(const TrainArgs &a, int block, unsigned char *lds) {
     using S = Shape<TM>;
     const WeightTiles wt = weight_tiles<TM>(a.E, a.dw1 != nullptr, a.dw2 != nullptr, a.H, a.I);
     const int tid = threadIdx.x, lane = tid & 63;
@@ -723,7 +732,7 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs &a, int block, 
 constexpr int waves_per_simd(int TM) { return TM == 256 ? 2 : 4; }
 
 template <int TM>
-__global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_glu_kernel(GradArgs a) {
+__global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_glu_kernel(TrainArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<TM>::kLds];
     row_product<Gemm::kGradGlu, TM>(a, blockIdx.x, lds);
 }
@@ -731,11 +740,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_glu_kernel(
 // The forward for training of the layers that take small tiles (large ones run the forward's own kernels, whose 64-k
 // stages fetch whole cache lines of both operands: T = 4096, H = 2048, I = 1408, E = 64, k = 6 takes 530 us there and
 // 593 us with these products in 256 x 256 tiles).
-__global__ __launch_bounds__(kThreads, waves_per_simd(128)) void forward_glu_kernel(GradArgs a) {
+__global__ __launch_bounds__(kThreads, waves_per_simd(128)) void forward_glu_kernel(TrainArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<128>::kLds];
     row_product<Gemm::kFwdGlu, 128>(a, blockIdx.x, lds);
 }
-__global__ __launch_bounds__(kThreads, waves_per_simd(128)) void forward_out_kernel(GradArgs a) {
+__global__ __launch_bounds__(kThreads, waves_per_simd(128)) void forward_out_kernel(TrainArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<128>::kLds];
     row_product<Gemm::kFwdOut, 128>(a, blockIdx.x, lds);
 }
@@ -744,7 +753,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(128)) void forward_out_ker
 // the small layers pay one launch's latency for three, and the large ones fill one product's last round of
 // workgroups with the next one's tiles (the weight gradients' smallest tiles come last).
 template <int TM>
-__global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_products_kernel(GradArgs a, int in_blocks) {
+__global__ __launch_bounds__(kThreads, waves_per_simd(TM)) void grad_products_kernel(TrainArgs a, int in_blocks) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<TM>::kLds];
     if ((int)blockIdx.x < in_blocks)
         row_product<Gemm::kGradIn, TM>(a, blockIdx.x, lds);
@@ -759,7 +768,7 @@ int64_t row_blocks(int64_t max_tiles, int nb_n) {
 }
 
 template <int TM>
-hipError_t launch(const GradArgs &a, const moe_problem &p, int32_t *tiles, int32_t *n_tiles, int4 *order, hipStream_t s) {
+hipError_t launch(const TrainArgs &a, const moe_problem &p, int32_t *tiles, int32_t *n_tiles, int4 *order, hipStream_t s) {
     const int64_t max_tiles = grad_max_tiles(p, TM);
     hipLaunchKernelGGL(grad_prepare_kernel, dim3(1), dim3(256), 0, s, a.offsets, p.E, TM, tiles, n_tiles, order);
     hipError_t e = hipGetLastError();
@@ -777,7 +786,7 @@ hipError_t launch_grouped_grad_bf16(const uint16_t *dy, const uint16_t *x, const
                                     const moe_weights &w, const moe_problem &p, int32_t *tiles, int32_t *n_tiles,
                                     int32_t *order, uint16_t *dgu, uint16_t *h, uint16_t *dx, uint16_t *dw1,
                                     uint16_t *dw2, hipStream_t s) {
-    const GradArgs a = {offsets, tiles, n_tiles, (const int4 *)order, p.E, p.H, p.I, dy, x, (const uint16_t *)w.w1,
+    const TrainArgs a = {offsets, tiles, n_tiles, (const int4 *)order, p.E, p.H, p.I, dy, x, (const uint16_t *)w.w1,
                         (const uint16_t *)w.w2, gu, dgu, h, dx, dw1, dw2, p.glu_interleave, p.swiglu_clamp};
     return small_tiles(p) ? launch<128>(a, p, tiles, n_tiles, (int4 *)order, s)
                           : launch<256>(a, p, tiles, n_tiles, (int4 *)order, s);
@@ -791,7 +800,7 @@ hipError_t launch_ffn_train_small_bf16(const uint16_t *x, const int32_t *offsets
                                        const moe_problem &p, int32_t *list, uint16_t *gu, uint16_t *h, uint16_t *y,
                                        hipStream_t s) {
     constexpr int TM = 128;
-    GradArgs a = {};
+    TrainArgs a = {};
     int32_t *n_tiles = list, *tiles = list + 4;
     a.offsets = offsets, a.tiles = tiles, a.n_tiles = n_tiles, a.E = p.E, a.H = p.H, a.I = p.I;
     a.x = x, a.w1 = (const uint16_t *)w.w1, a.w2 = (const uint16_t *)w.w2, a.dgu = gu, a.h = h, a.dx = y;
