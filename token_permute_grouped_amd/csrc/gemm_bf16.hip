@@ -112,13 +112,8 @@ __device__ __forceinline__ void interleave_x_ds_mfma() {
 
 }  // namespace
 
-enum class Gemm {
-    kGlu,      // GEMM1 + SwiGLU -> h
-    kGluKeep,  // the same, with the pre-activations stored too
-    kOut,      // GEMM2 -> y
-};
-
-template <Gemm kKind>
+// kKeep (with kSwiGLU): the pre-activations are stored too
+template <bool kSwiGLU, bool kKeep = false>
 __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     const uint16_t *__restrict__ A,        // [S][K] activations in expert-contiguous row order, or
                                            // with row_src: the token rows [a_rows][K]
@@ -131,8 +126,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     int K, int N, int I, int il, float clamp,
     uint16_t *__restrict__ C, int ldc,     // [S][ldc]
     const int32_t *__restrict__ row_dst,   // NULL, or [S]: row r of the tile order is stored to row row_dst[r] of C
-    uint16_t *__restrict__ gu) {           // kGluKeep: [S][2I], the pre-activations
-    constexpr bool kSwiGLU = kKind != Gemm::kOut;
+    uint16_t *__restrict__ gu) {           // kKeep: [S][2I], the pre-activations
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kBBase + kBStages * kBStage];  // 160 KB
 
     // ---- tile of this workgroup: band of m-tiles, XCD rectangle within the band, tile within it
@@ -409,7 +403,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
     auto cofs = [](int r, int c) { return r * (kCols * 2) + ((c ^ (r & 15)) << 4); };
     const int half = lane >> 5;
     lds_barrier();  // every wave is done with the last stage's operands
-    if constexpr (kKind == Gemm::kGluKeep) {
+    if constexpr (kKeep) {
         // the pre-activations first, a 256-column bf16 tile in W1's stored row order: a contiguous
         // run of 256 (interleaved rows), or 128 gate and 128 up columns I apart
         auto gofs = [](int r, int c) { return r * (kBN * 2) + ((c ^ (r & 15)) << 4); };
@@ -478,7 +472,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_bf16_kernel(
 }
 
 namespace {
-template <Gemm kKind>
+template <bool kSwiGLU, bool kKeep = false>
 hipError_t launch(const uint16_t *A, const int32_t *row_src, int gather_k, int a_rows, const uint16_t *W,
                   const int32_t *offsets, const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int K,
                   int N, int I, int il, float clamp, uint16_t *C, int ldc, const int32_t *row_dst, hipStream_t s,
@@ -486,21 +480,20 @@ hipError_t launch(const uint16_t *A, const int32_t *row_src, int gather_k, int a
     const int nb_n = (N + kBN - 1) / kBN;
     const TileMap tm = tile_map(nb_n);
     const int64_t blocks = (max_tiles + tm.gm - 1) / tm.gm * tm.per_band;
-    hipLaunchKernelGGL(grouped_gemm_bf16_kernel<kKind>, dim3(blocks), dim3(kThreads), 0, s, A, row_src, gather_k,
-                       a_rows, W, offsets, tiles, n_tiles, K, N, I, il, clamp, C, ldc, row_dst, gu);
+    hipLaunchKernelGGL((grouped_gemm_bf16_kernel<kSwiGLU, kKeep>), dim3(blocks), dim3(kThreads), 0, s, A, row_src,
+                       gather_k, a_rows, W, offsets, tiles, n_tiles, K, N, I, il, clamp, C, ldc, row_dst, gu);
     return hipGetLastError();
 }
 }  // namespace
 
 hipError_t launch_gemm1_swiglu_bf16(const uint16_t *x_perm, const uint16_t *w1, const int32_t *offsets,
                                     const int32_t *tiles, const int32_t *n_tiles, int64_t max_tiles, int H, int I,
-                                    int glu_interleave, float clamp, uint16_t *h, uint16_t *gu,
-                                    hipStream_t s) {
+                                    int glu_interleave, float clamp, uint16_t *h, uint16_t *gu, hipStream_t s) {
     if (gu)
-        return launch<Gemm::kGluKeep>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
-                                      glu_interleave, clamp, h, I, nullptr, s, gu);
-    return launch<Gemm::kGlu>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
-                              glu_interleave, clamp, h, I, nullptr, s);
+        return launch<true, true>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I,
+                                  glu_interleave, clamp, h, I, nullptr, s, gu);
+    return launch<true>(x_perm, nullptr, 1, 0, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I, glu_interleave,
+                        clamp, h, I, nullptr, s);
 }
 
 hipError_t launch_gemm1_swiglu_gather_bf16(const uint16_t *x, const int32_t *row_src, int T, int k,
@@ -508,15 +501,15 @@ hipError_t launch_gemm1_swiglu_gather_bf16(const uint16_t *x, const int32_t *row
                                            const int32_t *n_tiles, int64_t max_tiles, int H, int I,
                                            int glu_interleave, float clamp, uint16_t *h, hipStream_t s) {
     if (!gather_fits(T, H)) return hipErrorInvalidValue;
-    return launch<Gemm::kGlu>(x, row_src, k, T, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I, glu_interleave,
-                              clamp, h, I, nullptr, s);
+    return launch<true>(x, row_src, k, T, w1, offsets, tiles, n_tiles, max_tiles, H, 2 * I, I, glu_interleave, clamp,
+                        h, I, nullptr, s);
 }
 
 hipError_t launch_gemm2_bf16(const uint16_t *h, const uint16_t *w2, const int32_t *offsets, const int32_t *tiles,
                              const int32_t *n_tiles, int64_t max_tiles, int H, int I, uint16_t *y_perm,
                              const int32_t *row_dst, hipStream_t s) {
-    return launch<Gemm::kOut>(h, nullptr, 1, 0, w2, offsets, tiles, n_tiles, max_tiles, I, H, I, 0, 0.0f, y_perm, H,
-                              row_dst, s);
+    return launch<false>(h, nullptr, 1, 0, w2, offsets, tiles, n_tiles, max_tiles, I, H, I, 0, 0.0f, y_perm, H, row_dst,
+                         s);
 }
 
 }  // namespace tpg
