@@ -101,10 +101,10 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 
 // 16 bytes per lane from the buffer to LDS address dst + 16 lane.  (m0 is a reserved register, which nothing
 // else in these kernels uses, so it is not and may not be named as clobbered.)
-__device__ __forceinline__ void dma(i32x4 rsrc, uint32_t voff, int soff, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+__device__ __forceinline__ void dma(i32x4 rsrc, uint32_t voff, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(dst), "v"(voff), "s"(rsrc), "s"(soff));
+                 : "s"(dst), "v"(voff), "s"(rsrc));
 }
 
 // k on the rows: the logical 16-byte chunk that chunk position p of row r holds
@@ -266,24 +266,27 @@ __device__ __forceinline__ void row_product(const TrainArgs &a, int block, unsig
         offP[i] = pr < live ? (uint32_t)(pr * K + c * 8) * 2u : 0x80000000u;
     }
     const uint32_t lds0 = lds_address(lds);
-    // the next stage's offsets in P's rows and in Q; behind the last one nothing is in bounds
-    const uint16_t *p0 = P + (row0 + m0) * K, *q0 = Q + (int64_t)e * K * N;
-    int sp = 0, sq = 0, np = live * K * 2, nq = K * N * 2;
+    // The next stages' addresses and how many stages are left; behind the last one nothing is in bounds.  (The
+    // bounds of a buffer are compared after its scalar offset is taken from them, in unsigned arithmetic: an empty
+    // buffer keeps everything out only if that offset is 0, so the addresses move instead.)
+    const char *rp = (const char *)(P + (row0 + m0) * K), *rq = (const char *)(Q + (int64_t)e * K * N);
+    int left_p = kFwd ? nk : nk / 2, left_q = nk;
+    const int bytes_p = live * K * 2, bytes_q = K * N * 2;
     auto request_p = [&](uint32_t dst) {
         dst += wave * (kOpsP * 1024);
-        const i32x4 rp = buffer(p0, np);
+        const i32x4 b = buffer(rp, left_p > 0 ? bytes_p : 0);
 #pragma unroll
-        for (int i = 0; i < kOpsP; ++i) dma(rp, offP[i], sp, dst + i * 1024);
-        sp += kFwd ? kBK * 2 : kBK * 4;
-        if (sp == K * 2) np = 0;
+        for (int i = 0; i < kOpsP; ++i) dma(b, offP[i], dst + i * 1024);
+        rp += kFwd ? kBK * 2 : kBK * 4;
+        --left_p;
     };
     auto request_q = [&](uint32_t dst) {
         dst += wave * (S::kOps * 1024);
-        const i32x4 rq = buffer(q0, nq);
+        const i32x4 b = buffer(rq, left_q > 0 ? bytes_q : 0);
 #pragma unroll
-        for (int i = 0; i < S::kOps; ++i) dma(rq, offQ[i], sq, dst + i * 1024);
-        sq += kFwd ? kBK * 2 : kBK * 2 * N;
-        if (sq == (kFwd ? K * 2 : K * N * 2)) nq = 0;
+        for (int i = 0; i < S::kOps; ++i) dma(b, offQ[i], dst + i * 1024);
+        rq += kFwd ? kBK * 2 : (int64_t)kBK * 2 * N;
+        --left_q;
     };
 
     f32x16 acc[S::kNX][S::kNB];
@@ -613,8 +616,8 @@ __device__ __forceinline__ void grad_weight_tiles(const TrainArgs &a, int block,
         const i32x4 p = buffer(rp, n > 0 ? (n - 1) * ldp2 + rows2 : 0), q = buffer(rq, n > 0 ? (n - 1) * ldq2 + cols2 : 0);
 #pragma unroll
         for (int i = 0; i < S::kOps; ++i) {
-            dma(p, vp[i], 0, dst + i * 1024);
-            dma(q, vq[i], 0, dst + S::kHalf + i * 1024);
+            dma(p, vp[i], dst + i * 1024);
+            dma(q, vq[i], dst + S::kHalf + i * 1024);
         }
         rp += (int64_t)kBK * ldp2;
         rq += (int64_t)kBK * ldq2;
