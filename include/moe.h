@@ -338,7 +338,7 @@ enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
  * `const moe_residual *`, NULL means neither. */
 typedef struct moe_residual {
     const void *x;      /* bf16 [T][H], or NULL: no residual */
-    float scale;        /* multiplies the residual; finite */
+    float scale;        /* multiplies the residual; finite.  Unused without one */
     const float *gate;  /* fp32 [H] (MOE_GATE_CHANNEL) or [T] (MOE_GATE_TOKEN); unused for MOE_GATE_NONE */
     int32_t gate_kind;
 } moe_residual;

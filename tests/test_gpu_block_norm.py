@@ -226,6 +226,17 @@ def test_combine_norm_backward(T, H, E, k, drop, form, gate, residual):
     assert torch.equal(again[:R], dy[:R])
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf")])
+def test_scale_of_no_residual_is_not_used(scale):
+    T, H = 9, 256
+    c = _end_problem(T, H, 4, 2, 0.3, "token", "norm", False, seed=4)
+    y, slot_row, tw, _, _, gate = c["keep"]
+    out, want = nan(T, H), nan(T, H)
+    for s, o in ((scale, out), (1.0, want)):
+        tpg.moe_combine_norm(y, slot_row, tw, c["norm"], tpg.make_residual(None, s, gate, tpg.MOE_GATE_TOKEN), c["p"], o)
+    assert torch.isfinite(want).all() and torch.equal(out, want)
+
+
 @pytest.mark.parametrize("T,H,k", [(5, 640, 1), (40, 4096, 1), (33, 256, 3), (2, 16512, 1), (7, 384, 9)])
 def test_weight_gradient_of_a_token_with_one_live_slot(T, H, k):
     """the norm takes a single weight out again but for eps: dtopk_w = r^3 eps (b . y), a difference of two numbers

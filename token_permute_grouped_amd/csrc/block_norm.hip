@@ -706,7 +706,8 @@ NormArgs norm_args(const moe_norm *n, int H) {
 }
 ResidualArgs residual_args(const moe_residual *r) {
     if (!r) return {nullptr, 0.f, nullptr, MOE_GATE_NONE};
-    return {(const uint4 *)r->x, r->scale, r->gate, r->gate_kind};
+    // without a residual its scale is not looked at, and would make a NaN of infinity times nothing
+    return {(const uint4 *)r->x, r->x ? r->scale : 0.f, r->gate, r->gate_kind};
 }
 }  // namespace
 
