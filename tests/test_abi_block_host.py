@@ -88,6 +88,14 @@ def test_misaligned_rows(call, odd):
     _refused(UNSUPPORTED, fn, *[ODD if i == odd else a for i, a in enumerate(args)])
 
 
+def test_misaligned_sums_over_tokens():
+    p, norm, res = _p(), tpg.Norm(F, 1e-6), tpg.Residual(None, 1.0, F, tpg.MOE_GATE_CHANNEL)
+    _refused(UNSUPPORTED, tpg.moe_prenorm_backward, F, F, None, None, F, norm, p, F, ODD, F, BIG)
+    _refused(UNSUPPORTED, tpg.moe_prenorm_backward, F, F, None, None, F, norm, p, F, F, ODD, BIG)
+    for dw, dg, ws in ((ODD, F, F), (F, ODD, F), (F, F, ODD)):
+        _refused(UNSUPPORTED, tpg.moe_combine_norm_backward, F, F, F, F, norm, res, p, F, F, None, dw, dg, ws, BIG)
+
+
 def test_gradients_of_what_is_not_there():
     p, norm, res = _p(), tpg.Norm(F, 1e-6), tpg.Residual(None, 1.0, None, 0)
     _refused(UNSUPPORTED, tpg.moe_prenorm_backward, F, F, None, None, F, None, p, F, F, F, BIG)

@@ -506,7 +506,8 @@ int moe_prenorm_backward(const void *dx_perm, const int32_t *slot_row, const voi
     if (!dx || (!dx_perm && !dxn) || (dx_perm && !slot_row) || (norm && !x)) return MOE_ERR_NULL;
     if (dweight && !norm) return MOE_ERR_UNSUPPORTED;
     if (dweight && !ws) return MOE_ERR_NULL;
-    if ((st = check_norm(norm)) || (st = check_aligned(dx_perm, dxn, dres, norm ? x : nullptr, dx, dweight, ws)))
+    if ((st = check_norm(norm)) || (st = check_aligned(dx_perm, dxn, dres, norm ? x : nullptr, dx, dweight,
+                                                   dweight ? ws : nullptr)))
         return st;
     if (dweight && ws_bytes < partial_bytes(*p)) return MOE_ERR_WORKSPACE;
     return hip_status(launch_prenorm_backward(dx_perm, slot_row, dxn, dres, x, norm, *p, dx, dweight, (float *)ws,
@@ -541,7 +542,9 @@ int moe_combine_norm_backward(const void *dout, const void *y_perm, const int32_
         return MOE_ERR_UNSUPPORTED;
     const bool partials = dweight || (dgate && gate_kind == MOE_GATE_CHANNEL);
     if (partials && !ws) return MOE_ERR_NULL;
-    if ((st = check_aligned(dout, y_perm, dy_perm, dresidual, ws))) return st;
+    if ((st = check_aligned(dout, y_perm, dy_perm, dresidual, dweight,
+                            gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr, partials ? ws : nullptr)))
+        return st;
     if (partials && ws_bytes < partial_bytes(*p)) return MOE_ERR_WORKSPACE;
     return hip_status(launch_combine_norm_backward(dout, y_perm, slot_row, topk_w, norm, residual, *p, dy_perm, dtopk_w,
                                                    dresidual, dweight, dgate, (float *)ws, stream));
