@@ -317,3 +317,81 @@ def test_more_tokens_than_one_grid_dimension_holds():
     c = x.double().flip(0) * w.double()
     ref = c * torch.rsqrt(c.square().mean(1, keepdim=True) + EPS)
     assert bool(((out.double() - ref).abs() <= (HALF + FP32) * ref.abs()).all())
+
+
+@pytest.mark.parametrize("T,H,E,k", [(700, 384, 8, 2), (5, 7168, 12, 9), (3, 16512, 4, 2)])
+def test_gradients_over_their_inputs(T, H, E, k):
+    """dx may be dres, dxn or x; dresidual may be dout, with dy over y at the same time"""
+    g = _gen(T, H, k, 2)
+    p = _problem(T, H, E, k)
+    _, slot_row, _ = routing(T, E, k, g, 0.1)
+    dxp, dxn, dres, x = (dev(bf16(n, H, g=g)) for n in (T * k, T, T, T))
+    sr, norm = dev(slot_row), tpg.make_norm(dev(bf16(H, g=g)), EPS)
+    ws = workspace(p, tpg.MOE_WS_PRENORM_BACKWARD)
+    want, dw = nan(T, H), nan(H, dtype=torch.float32)
+    tpg.moe_prenorm_backward(dxp, sr, dxn, dres, x, norm, p, want, dw, ws)
+    assert torch.isfinite(want).all()
+    for i in range(3):
+        a = [t.clone() for t in (dxn, dres, x)]
+        dw2 = nan(H, dtype=torch.float32)
+        tpg.moe_prenorm_backward(dxp, sr, *a, norm, p, a[i], dw2, ws)
+        assert torch.equal(a[i], want) and torch.equal(dw2, dw), i
+
+    c = _end_problem(T, H, E, k, 0.1, "channel", "norm", True, seed=2)
+    dout = dev(bf16(T, H, g=g))
+    y, slot_row, tw = c["keep"][:3]
+    ws = workspace(p, tpg.MOE_WS_COMBINE_NORM_BACKWARD)
+
+    def run(dout, y, dy, dres):
+        o = [nan(T, k, dtype=torch.float32), nan(H, dtype=torch.float32), nan(H, dtype=torch.float32)]
+        tpg.moe_combine_norm_backward(dout, y, slot_row, tw, c["norm"], c["residual"], p, dy, o[0], dres, o[1], o[2], ws)
+        return [dy[:c["R"]], dres] + o
+
+    want = run(dout, y, nan(T * k, H), nan(T, H))
+    d2, y2 = dout.clone(), y.clone()
+    for a, b in zip(run(d2, y2, y2, d2), want):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("prec", ["bf16", "w4a8"])
+@pytest.mark.parametrize("T", [3, 600])
+def test_block_forward_in_place_and_in_a_graph(prec, T):
+    """prenorm and the block behind it, out over the residual, on another stream and captured with the steps of
+    another problem between the replays"""
+    cfg = MoeConfig("norm_graph", T=T, H=512, I=256, E=8, k=2, prec=prec, drop_p=0.2)
+    d = DeviceProblem(generate(cfg, seed=T))
+    g = _gen(T, 9)
+    w, gate = dev(bf16(512, g=g)), dev(torch.randn(512, generator=g))
+    x0 = dev(bf16(T, 512, g=g))
+    x = x0.clone()
+    norm, rd = tpg.make_norm(w, EPS), tpg.make_residual(x, 0.5, gate, tpg.MOE_GATE_CHANNEL)
+    ws = d.workspace(tpg.MOE_WS_FORWARD, fill=0xEF)
+    bf = prec == "bf16"
+    xn = nan(T, 512) if bf else torch.zeros(T, 512, dtype=torch.uint8, device=DEV)
+    sc = None if bf else nan(T, 4, dtype=torch.float32)
+
+    def run(out):
+        tpg.moe_prenorm(x, norm, d.p, xn if bf else None, None if bf else xn, sc)
+        tpg.moe_forward_norm(d.logits, d.drop, xn, sc, d.weights, norm, rd, d.p, out, ws)
+
+    want = nan(T, 512)
+    run(want)
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all() and torch.equal(x, x0)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(x)
+    torch.cuda.synchronize()
+    assert torch.equal(x, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(x)
+    other = nan(70, 640)
+    for _ in range(4):
+        x.copy_(x0)
+        ws.fill_(0xEF)
+        tpg.moe_prenorm(dev(bf16(70, 640, g=g)), None, _problem(70, 640), other)  # eager work between the replays
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x, want)

@@ -346,6 +346,32 @@ def test_training_step_is_reproducible_captured_and_on_another_stream():
         check(f"replay {i}")
 
 
+@pytest.mark.parametrize("counts,H,I", [([600, 0, 300], 384, 256), ([40] * 200, 256, 128)])
+def test_two_captured_backward_passes_share_a_workspace(counts, H, I):
+    """small and large tiles; the passes follow one another on one stream, each writes what it reads of the workspace"""
+    a, b = (Ffn(counts, H, I, il=32, clamp=3.0, seed=i) for i in range(2))
+    ws = workspace(a.p, tpg.MOE_WS_FFN_BACKWARD)
+    dev_in = [[dev(t) for t in (f.dy, f.x, f.gu, f.offsets)] for f in (a, b)]
+    outs = [[nan(f.S, H), nan(len(counts), 2 * I, H), nan(len(counts), H, I)] for f in (a, b)]
+    want = [f.backward() for f in (a, b)]
+    torch.cuda.synchronize()
+    graphs = []
+    for f, i, o in zip((a, b), dev_in, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            tpg.moe_grouped_ffn_backward(*i, f.weights, f.p, *o, ws)
+    for n in range(3):
+        ws.fill_(0xFF)
+        for o in outs[0] + outs[1]:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for gr in graphs[::-1] if n == 1 else graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs[0] + outs[1], want[0] + want[1]):
+            assert torch.equal(o.view(torch.int16), w.view(torch.int16)), n
+
+
 def test_two_steps_at_once_on_two_streams():
     a, b = Step(seed=7), Step(T=150, H=384, seed=8)
     for s in (a, b):
