@@ -52,11 +52,20 @@ __device__ __forceinline__ float silu_mul(float g, float u, float clamp) {
 // columns of n-tiles, about 32 tiles each: one per CU of an XCD), and XCD x takes
 // rectangle x.  The 32 tiles an XCD runs at once then share ~8 activation slabs and ~4
 // weight slabs in its L2, and all XCDs stay on one band (a few experts) in the MALL.
+//
+// Four columns of rectangles, or two or one if that leaves fewer columns without tiles (their XCDs would idle: with 6
+// n-tiles two of the eight) and a rectangle still has two m-tiles that share its weights.  Times with four columns
+// always / so, 64 experts of 345 rows: 5 and 8 n-tiles (H = 2048, I = 640) forward 331 / 270 us; 11, 8 (I = 1408)
+// 513 / 485, backward pass (6, 8) 1072 / 1022; 19 n-tiles in one column of rectangles of one m-tile 469 / 507.
 struct TileMap {
     int xn, nc, gm, per_band;  // rectangle columns, n-tiles per column, band m-tiles, workgroups per band
 };
-__host__ __device__ inline TileMap tile_map(int nb_n) {
-    const int xn = nb_n >= 4 ? 4 : nb_n >= 2 ? 2 : 1;
+__host__ __device__ inline TileMap tile_map(int nb_n, int min_xn = 1) {
+    int xn = nb_n >= 4 ? 4 : nb_n >= 2 ? 2 : 1;
+    for (int c = xn / 2; c >= min_xn; c /= 2) {
+        const int nc = (nb_n + c - 1) / c;
+        if (nc <= 16 && c * nc < xn * ((nb_n + xn - 1) / xn)) xn = c;
+    }
     const int nc = (nb_n + xn - 1) / xn;
     const int rm = 32 / nc > 1 ? 32 / nc : 1;  // m-tiles per rectangle
     return {xn, nc, (8 / xn) * rm, 8 * rm * nc};
@@ -67,8 +76,9 @@ __host__ __device__ inline TileMap tile_map(int nb_n) {
 // partial m-tile per expert.  A partial tile does little MFMA work for the weights it streams, so
 // partial tiles are spread evenly through the order (position v is partial when floor(v P / n) steps) and
 // their weight streaming overlaps the full tiles' MFMAs instead of forming a memory-bound tail.
-__device__ __forceinline__ bool row_tile(int block, int nb_n, const int32_t *__restrict__ n_tiles, int &mt, int &nt) {
-    const TileMap tm = tile_map(nb_n);
+__device__ __forceinline__ bool row_tile(int block, int nb_n, const int32_t *__restrict__ n_tiles, int &mt, int &nt,
+                                         int min_xn = 1) {
+    const TileMap tm = tile_map(nb_n, min_xn);
     const int n_mt = n_tiles[0];
     const int band = block / tm.per_band, p = block % tm.per_band;
     const int first_m = band * tm.gm;
