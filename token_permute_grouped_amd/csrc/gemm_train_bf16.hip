@@ -724,8 +724,10 @@ __device__ __forceinline__ void grad_weight_tiles(const TrainArgs &a, int block,
                 for (int i = 0; i < 64 / (kWaves * S::kLines); ++i) {
                     const int r = (i * kWaves + wave) * S::kLines + lane / S::kChunks;
                     const int row = (r >> 5) * S::kRows + b * 32 + (r & 31);
+                    // past the L2: nothing here reads it, and the operands stay (64 experts of 8 rows 454 -> 388 us)
                     if (row < done.rows)
-                        *(u32x4 *)(done.C + (int64_t)row * done.N + ch * 8) = *(const u32x4 *)(st + cofs(r, ch));
+                        __builtin_nontemporal_store(*(const u32x4 *)(st + cofs(r, ch)),
+                                                    (u32x4 *)(done.C + (int64_t)row * done.N + ch * 8));
                 }
             }
         }
