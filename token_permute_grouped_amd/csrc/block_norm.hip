@@ -18,7 +18,7 @@
 //
 // Measured, T = 16384, H = 4096, k = 8, a tenth of the slots dropped (a 1 GiB copy moves 5.1 TB/s): prenorm to bf16 46
 // us (5.8 TB/s); its gradient with router and residual gradients 290 us (5.2 TB/s; 400 us before the next token's rows
-// were requested ahead of this one's reduction); combine backward 451 us (4.9 TB/s; 636 us when it read every row
+// were requested ahead of this one's reduction); combine backward 438 us (5.0 TB/s; 636 us when it read every row
 // twice and reduced twice).  One token of H = 7168: 3-5 us a kernel, the launch.
 //
 // The sums over tokens (dweight, dgate of a channel gate) are kept in registers by workgroups that

@@ -27,8 +27,8 @@
 // Layers whose 256 x 256 tiles would leave CUs idle take 128 x 128 tiles in half the LDS, two workgroups per CU
 // (small_tiles).
 //
-// What bounds it.  The large layer's backward pass takes 13.5 ms, 0.98 PFLOP/s: the matrix cores are busy 63 % of the
-// cycles in the second launch (56 % in kGradGlu) at the 1.5 GHz that the board's power limit leaves (a library bf16
+// What bounds it.  The large layer's backward pass takes 13.0 ms, 1.02 PFLOP/s: the matrix cores are busy 65 % of the
+// cycles in the second launch (57 % in kGradGlu) at the 1.5 GHz that the board's power limit leaves (a library bf16
 // product of 16384^3 runs 1.35 PFLOP/s there with this operand order).  Experts of few rows are bound by the stores of
 // their weight gradients (128 experts of 32 rows, 6.4 GB of gradients: 2.0 ms with dx).
 //
